@@ -33,7 +33,9 @@ EXPORTED = ["nsa_sel_attn_workspace_size", "nsa_sel_attn_fwd", "nsa_sel_attn_bwd
             "nsa_sel_invert_index",
             "nsa_sel_invert_index_noalloc", "nsa_sel_invert_index_noalloc_max_bytes",
             "nsa_sel_invert_index_scratch_bytes",
-            "nsa_sel_validate_indices", "nsa_sel_check_status", "nsa_sel_status_string"]
+            "nsa_sel_validate_indices", "nsa_sel_paged_plan", "nsa_sel_paged_write_kv",
+            "nsa_sel_paged_attn_workspace_size", "nsa_sel_paged_attn_fwd", "nsa_sel_paged_sel_fwd",
+            "nsa_sel_check_status", "nsa_sel_status_string"]
 
 _lib = None
 _lock = threading.Lock()
@@ -93,6 +95,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.nsa_sel_invert_index_scratch_bytes.restype = Z
             lib.nsa_sel_validate_indices.argtypes = [P, I, I, I, P, I, I, P, P, P, Z, P]
             lib.nsa_sel_validate_indices.restype = I
+            L = ctypes.c_int64
+            lib.nsa_sel_paged_plan.argtypes = [P, P, I, P, I, P, I, L, I, I, P, P, P, P, P, P]
+            lib.nsa_sel_paged_plan.restype = I
+            lib.nsa_sel_paged_write_kv.argtypes = [P, P, L, L, L, L, P, I, P, P]
+            lib.nsa_sel_paged_write_kv.restype = I
+            lib.nsa_sel_paged_attn_workspace_size.argtypes = [I, I, I, I, I]
+            lib.nsa_sel_paged_attn_workspace_size.restype = Z
+            tail = [F, I, P, P, P, Z, P, ctypes.c_uint]
+            lib.nsa_sel_paged_attn_fwd.argtypes = [P, L, L, I, I, P, P, P, I, P, I, L] + tail
+            lib.nsa_sel_paged_attn_fwd.restype = I
+            lib.nsa_sel_paged_sel_fwd.argtypes = [P, L, L, I, I, P, P, P, I, P, I, L, P, I, I] + tail
+            lib.nsa_sel_paged_sel_fwd.restype = I
             lib.nsa_sel_check_status.argtypes = [P, P]
             lib.nsa_sel_check_status.restype = I
             lib.nsa_sel_status_string.argtypes = [I]
@@ -463,3 +477,7 @@ def selected_attention(q, k, v, cu_seqlens, block_idx, block_size=64, scale=None
     return SelectedAttention.apply(q, k, v, cu_seqlens, block_idx, block_size,
                                    float(q.shape[-1] ** -0.5 if scale is None else scale),
                                    int(window_size))
+
+
+from .paged import (nsa_sel_paged_attn_fwd, nsa_sel_paged_attn_workspace_size,  # noqa: E402
+                    nsa_sel_paged_plan, nsa_sel_paged_sel_fwd, nsa_sel_paged_write_kv)

@@ -125,6 +125,10 @@ Layout make_layout(const Dims& D, bool bwd) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+}  // namespace
+
+namespace nsa {
+
 // The current device must be an sm_100 part, and `stream` (when it is not one of the
 // default-stream handles) must belong to it: the launches, the scratch of the
 // no-allocation entry point and the SM count are all taken from the current device.
@@ -133,9 +137,15 @@ nsa_status_t check_device(int* num_sms, nsa_stream_t stream_) {
     if (cudaGetDevice(&dev) != cudaSuccess) return NSA_ERR_NO_DEVICE;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (stream != nullptr && stream != cudaStreamLegacy && stream != cudaStreamPerThread) {
-        int sdev = -1;
-        if (cudaStreamGetDevice(stream, &sdev) != cudaSuccess) return NSA_ERR_INVALID_ARG;
-        if (sdev != dev) return NSA_ERR_INVALID_ARG;
+        // cudaStreamGetDevice would end a capture; a stream that is being captured is
+        // compared by its first launch, which fails on another device
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return NSA_ERR_INVALID_ARG;
+        if (cap == cudaStreamCaptureStatusNone) {
+            int sdev = -1;
+            if (cudaStreamGetDevice(stream, &sdev) != cudaSuccess) return NSA_ERR_INVALID_ARG;
+            if (sdev != dev) return NSA_ERR_INVALID_ARG;
+        }
     }
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -160,6 +170,10 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
     });
     return fn;
 }
+
+}  // namespace nsa
+
+namespace {
 
 // Tensor map over a bf16 [T, hkv, 128] tensor; box = (64 columns, 1 head, bs keys),
 // 128-byte swizzle (the layout the tensor-core descriptors expect).

@@ -332,6 +332,120 @@ NSA_API nsa_status_t nsa_sel_bsfa_fwd(const void *q, const void *k, const void *
                                   const float *tau, void *out, float *lse, void *workspace,
                                   size_t workspace_bytes, nsa_stream_t stream);
 
+/* ------------------------------------------------------------------ paged K/V cache
+ * Serving: K and V of the running requests live in pages of page_size tokens, and a
+ * request's block table names its pages in order.  (The pages this library was specified
+ * from have no counterpart; layout and names follow the calls above.)  One step of a
+ * server is nsa_sel_paged_plan once, then per layer nsa_sel_paged_write_kv and one of the
+ * two attention calls.
+ *
+ * The cache of one layer: element (page, token in page, KV head, column) of K lies at
+ * k + page * page_stride + token * token_stride + head * head_stride + column, V likewise
+ * with the same strides.  Strides count elements of 16 bits and are multiples of 8;
+ * k and v are 16-byte aligned; columns are adjacent.  (A [num_pages, page_size, hkv,
+ * head_dim] tensor, the same with heads before tokens, and one half of a tensor holding K
+ * and V side by side are all described this way.)
+ *   page_size  16, 32, 64, 128 or 256; num_pages < 2^31
+ *   head_dim   64 or 128; 1 <= num_seqs <= 16384; total_tokens < 2^25 */
+typedef struct {
+    void *k, *v;
+    int64_t page_stride, token_stride, head_stride;
+    int num_pages, page_size, hkv, head_dim;
+} nsa_paged_cache_t;
+
+/* Block tables, slot maps and cumulative lengths of one step.  Request r holds
+ * cached_lens[r] tokens and brings new_lens[r] more (either may be 0; negative values
+ * count as 0).  It holds the pages block_table[r, 0 .. ceil(cached / page_size)) and takes
+ * the pages it needs beyond them from the front of free_pages, requests in order.
+ *   new_lens, cached_lens  int32 [num_seqs]
+ *   free_pages    int32 [num_free] page numbers in the order they are to be taken
+ *   block_table   int32 [num_seqs, table_width], row stride table_stride (elements): the
+ *                 entries of fresh pages are written, all others are left as they were
+ *   total_tokens  rows of slots and positions, >= the sum of new_lens (more: a padded
+ *                 batch)
+ *   cu_seqlens    int32 [num_seqs + 1] (written): exclusive prefix sums of new_lens
+ *   kv_lens       int32 [num_seqs] (written): cached_lens + new_lens
+ *   slots         int64 [total_tokens] (written): page * page_size + place in the page of
+ *                 the token's K/V row; -1 behind the last token, and where a page is
+ *                 missing (the free list or the table's row is too short, or the table
+ *                 holds a negative entry there)
+ *   positions     int32 [total_tokens] (written): the token's position in its sequence; 0
+ *                 behind the last token
+ *   pages_used    int32 [1] (written): pages the step needs from free_pages.  When it
+ *                 exceeds num_free the table entries of the missing pages are -1.
+ * Nothing may alias.  One kernel; no workspace. */
+NSA_API nsa_status_t nsa_sel_paged_plan(const int32_t *new_lens, const int32_t *cached_lens,
+                                        int num_seqs, const int32_t *free_pages, int num_free,
+                                        int32_t *block_table, int table_width,
+                                        int64_t table_stride, int page_size, int total_tokens,
+                                        int32_t *cu_seqlens, int32_t *kv_lens, int64_t *slots,
+                                        int32_t *positions, int32_t *pages_used,
+                                        nsa_stream_t stream);
+
+/* Writes the K and V rows of total_tokens tokens into their slots.
+ *   k, v   16-bit [total_tokens, hkv, head_dim] (the type is not looked at), columns
+ *          adjacent, strides in elements, multiples of 8; 16-byte aligned
+ *   slots  int64 [total_tokens]; rows whose slot lies outside [0, num_pages * page_size)
+ *          are not written.  Slots that are written must be distinct. */
+NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_t k_token_stride,
+                                            int64_t k_head_stride, int64_t v_token_stride,
+                                            int64_t v_head_stride, const int64_t *slots,
+                                            int total_tokens, const nsa_paged_cache_t *cache,
+                                            nsa_stream_t stream);
+
+/* Attention of each request's new tokens over its paged cache, the new tokens' own K/V
+ * already written.  The query at row t of request r (rows cu_seqlens[r] ..
+ * cu_seqlens[r + 1] of q, n of them) has position i = kv_lens[r] - n + t - cu_seqlens[r]
+ * and attends the keys j of its request with j <= i, j < kv_lens[r] and, for a window of
+ * W = window_size > 0 keys, j > i - W.  A query that sees no key (i < 0) gets out = 0,
+ * lse = -inf.  Rows of q outside [cu_seqlens[0], cu_seqlens[num_seqs]) are not read and
+ * their outputs are left as they were.
+ *   q            bf16 (fp16 with flags = NSA_F16) [total_tokens, hq, head_dim], columns
+ *                adjacent, strides in elements, multiples of 8; 16-byte aligned
+ *   hq           a multiple of cache->hkv, at most 128 query heads per KV head
+ *   cu_seqlens   int32 [num_seqs + 1]; kv_lens int32 [num_seqs]
+ *   block_table  int32 [num_seqs, table_width], row stride table_stride (elements).  Only
+ *                entries of pages that hold a visible key are used: those behind kv_lens
+ *                and those wholly before the window may hold anything.
+ *   out          the type of q, [total_tokens, hq, head_dim] contiguous (written)
+ *   lse          fp32 [hq, total_tokens] (written; natural log), or null
+ *   workspace    of nsa_sel_paged_attn_workspace_size() bytes, 256-byte aligned; calls
+ *                that may overlap on the GPU need a workspace each
+ * Cache rows that hold no visible key may hold anything, infinities and NaN too.  The
+ * scale must be positive and finite.  Other flag bits return NSA_ERR_INVALID_ARG.
+ * Device-side problems (nsa_sel_check_status): cu_seqlens decreasing or beyond
+ * total_tokens, kv_lens beyond the table's row, a used table entry outside [0, num_pages):
+ * NSA_ERR_BAD_INDEX, the outputs of that request undefined; no access leaves the cache. */
+NSA_API size_t nsa_sel_paged_attn_workspace_size(int total_tokens, int num_seqs, int hq, int hkv,
+                                                 int head_dim);
+NSA_API nsa_status_t nsa_sel_paged_attn_fwd(const void *q, int64_t q_token_stride,
+                                            int64_t q_head_stride, int total_tokens, int hq,
+                                            const nsa_paged_cache_t *cache,
+                                            const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                            int num_seqs, const int32_t *block_table,
+                                            int table_width, int64_t table_stride, float scale,
+                                            int window_size, void *out, float *lse,
+                                            void *workspace, size_t workspace_bytes,
+                                            nsa_stream_t stream, unsigned flags);
+
+/* Selected-block attention over the paged cache: as nsa_sel_paged_attn_fwd, with the keys
+ * of a (token, KV head g) further limited to the blocks of block_idx[t, g, :]
+ * (block_size keys each, numbered from the start of the request's sequence; block numbers
+ * below 0 or behind the query's own block select nothing).  Block numbers within one row
+ * must be distinct.
+ *   block_idx   int32 [total_tokens, hkv, topk], 1 <= topk <= 64
+ *   block_size  64 or 128 */
+NSA_API nsa_status_t nsa_sel_paged_sel_fwd(const void *q, int64_t q_token_stride,
+                                           int64_t q_head_stride, int total_tokens, int hq,
+                                           const nsa_paged_cache_t *cache,
+                                           const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                           int num_seqs, const int32_t *block_table,
+                                           int table_width, int64_t table_stride,
+                                           const int32_t *block_idx, int topk, int block_size,
+                                           float scale, int window_size, void *out, float *lse,
+                                           void *workspace, size_t workspace_bytes,
+                                           nsa_stream_t stream, unsigned flags);
+
 /* Synchronises `stream` and returns the device-side status of the last call that
  * used this workspace (NSA_OK, NSA_ERR_TIMEOUT or NSA_ERR_BAD_INDEX). */
 NSA_API nsa_status_t nsa_sel_check_status(const void *workspace, nsa_stream_t stream);
