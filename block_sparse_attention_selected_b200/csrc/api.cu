@@ -881,11 +881,12 @@ nsa_status_t nsa_sel_select_topk(const float* scores, const int32_t* cu_seqlens,
 nsa_status_t nsa_sel_check_status(const void* workspace, nsa_stream_t stream_) {
     if (!workspace || !aligned(workspace, 256)) return NSA_ERR_INVALID_ARG;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    int code = 0;
-    if (cudaMemcpyAsync(&code, workspace, sizeof(int), cudaMemcpyDeviceToHost, stream) !=
-            cudaSuccess ||
+    DevStatus st;
+    if (cudaMemcpyAsync(&st, workspace, sizeof(st), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
         cudaStreamSynchronize(stream) != cudaSuccess)
         return NSA_ERR_CUDA;
+    int code = st.code;
+    for (int i = 0; code == 0 && i < kMaxStatusCtas; ++i) code = st.cta_err[i];
     return static_cast<nsa_status_t>(code);
 }
 

@@ -257,6 +257,7 @@ struct PagedAttnArgs {
     float* lse;              // [hq, T] or null
     DevStatus* st;
 };
+size_t paged_attn_workspace(int d);   // bytes, the status block included
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, int f16, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_validate(const int32_t* cu, int nseq, int T, int hkv, const int32_t* bidx,

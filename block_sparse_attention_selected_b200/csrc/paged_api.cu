@@ -52,8 +52,8 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     DevStatus* st = static_cast<DevStatus*>(ws);
-    if (cudaMemsetAsync(st, 0, sizeof(DevStatus), stream) != cudaSuccess) return NSA_ERR_CUDA;
-    if (T == 0) return NSA_OK;
+    if (T == 0)
+        return cudaMemsetAsync(st, 0, sizeof(DevStatus), stream) == cudaSuccess ? NSA_OK : NSA_ERR_CUDA;
     PagedAttnArgs p{};
     p.q = static_cast<const uint16_t*>(q);
     p.q_token_stride = q_token_stride;
@@ -176,7 +176,7 @@ size_t nsa_sel_paged_attn_workspace_size(int total_tokens, int num_seqs, int hq,
     if (total_tokens < 0 || num_seqs < 1 || hq < 1 || hkv < 1 || hq % hkv != 0) return 0;
     if (total_tokens >= (1 << 25) || num_seqs > kMaxSeqs || hq / hkv > kMaxGroup) return 0;
     if ((head_dim != 64 && head_dim != 128) || (long long)total_tokens * hq >= (1ll << 31)) return 0;
-    return sizeof(DevStatus);
+    return paged_attn_workspace(head_dim);
 }
 
 nsa_status_t nsa_sel_paged_attn_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,

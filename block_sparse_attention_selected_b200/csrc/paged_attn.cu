@@ -1,6 +1,40 @@
 // paged_attn.cu -- attention of new tokens over a paged K/V cache, over all of the
 // visible keys or over the key blocks that each (token, KV head) selects.
+//
+// Mathematics: one pass over the visible keys of a tile of query rows, 128 keys at a
+// time, S = Q K^T, P = 2^(c S - m), O += P V, with the running reference m of each row and
+// the sum l of its weights (c = scale log2 e).  m follows the row's maximum lazily: O and
+// l are rescaled only when the maximum has grown by more than 2^8 (kLazy), so that P stays
+// below 2^8 and fp32 sums lose nothing.  P is rounded to the 16-bit type of V for the
+// second product; l sums the unrounded weights.
+//
+// Work.  A unit is the rows of one KV head's query heads for up to NQ * floor(128 / G)
+// consecutive new tokens of one request (G query heads per KV head, rows token-major).
+//   all keys         the (unit, key tile) pairs of all units form one line that is cut into
+//                    one equal piece per CTA (one CTA per SM), whatever the lengths are; a
+//                    unit cut by a piece's end leaves fp32 partial results that
+//                    k_paged_merge joins in a fixed order.
+//   selected blocks  a unit is one token and walks the list of its valid blocks; units go
+//                    round the CTAs, and with fewer units than SMs each is split.
+// Two streams of (S, P, O) alternate on the tensor pipe, so that one stream's softmax runs
+// under the other's products:
+//   NQ = 2  two tiles of 128 query rows over the same key tiles (long chunks);
+//   NQ = 1  one tile of query rows, even and odd key tiles, joined when the unit ends
+//           (single tokens and short chunks: K and V are read once from memory, which
+//           bounds them).
+//
+//   warps 0-7    softmax, one warpgroup per stream, one thread per query row; epilogue
+//   warp 8       TMA producer: Q tiles, K and V tiles page by page through the block table
+//   warp 9       MMA issuer
+//   warp 10      scheduler: walks the CTA's pieces of work ahead of the others and hands
+//                them over through a ring in shared memory
+//
+// Keys that no row of a unit may see are never read into a product: their pages are not
+// loaded, and the issuer leaves out the 16-key steps of P V without a visible key and
+// clears the dead rows of V in the others (0 times infinity is not 0).
 #include <math_constants.h>
+
+#include <algorithm>
 
 #include "nsa_common.cuh"
 #include "nsa_kernels.h"
@@ -8,74 +42,1090 @@
 namespace nsa {
 namespace {
 
-template <int F16, int D>
-__global__ void __launch_bounds__(256) k_paged_rows(PagedAttnArgs p) {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= p.T * p.hq) return;
-    const int t = row / p.hq, h = row - t * p.hq, g = h / p.G;
-    if (t < __ldg(p.cu) || t >= __ldg(p.cu + p.R)) return;
-    const int r = seq_of_token(p.cu, p.R, t);
-    const int qlen = __ldg(p.cu + r + 1) - __ldg(p.cu + r);
-    if ((qlen < 0 || __ldg(p.cu + r + 1) > p.T) && lane == 0)
-        record_error(p.st, NSA_ERR_BAD_INDEX, 202, r);
-    const int kvlen = __ldg(p.kv_lens + r);
-    if (kvlen > p.table_width * p.ps && lane == 0) record_error(p.st, NSA_ERR_BAD_INDEX, 200, r);
-    const int kv = min(max(kvlen, 0), p.table_width * p.ps);
-    const int pos = kv - qlen + t - __ldg(p.cu + r);
-    constexpr int E = D / 32;
-    float q[E], o[E];
-    const uint16_t* qp = p.q + t * p.q_token_stride + h * p.q_head_stride + lane * E;
-    auto cvt = [](uint16_t x) { return F16 ? __half2float(__ushort_as_half(x)) : __bfloat162float(__ushort_as_bfloat16(x)); };
-    for (int e = 0; e < E; ++e) { q[e] = cvt(qp[e]); o[e] = 0.f; }
-    float m = -CUDART_INF_F, l = 0.f;
-    auto key = [&](int j) {
-        const int page = __ldg(p.table + (size_t)r * p.table_stride + j / p.ps);
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) record_error(p.st, NSA_ERR_BAD_INDEX, 201, r, j);
-            return;
-        }
-        const size_t at = page * p.page_stride + (j % p.ps) * p.token_stride + g * p.head_stride + lane * E;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s += q[e] * cvt(p.k[at + e]);
-        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= p.scale_log2;
-        const float mx = fmaxf(m, s), a = ex2_approx(m - mx), w = ex2_approx(s - mx);
-        l = l * a + w;
-        m = mx;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * cvt(p.v[at + e]);
-    };
-    const int lo = p.swin > 0 ? max(0, pos - p.swin + 1) : 0, hi = min(pos, kv - 1);
-    if (p.bidx) {
-        for (int s = 0; s < p.topk; ++s) {
-            const int b = __ldg(p.bidx + ((size_t)t * p.hkv + g) * p.topk + s);
-            if (b < 0 || b > hi / p.bs) continue;
-            for (int j = max(lo, b * p.bs); j <= min(hi, b * p.bs + p.bs - 1); ++j) key(j);
-        }
-    } else {
-        for (int j = lo; j <= hi; ++j) key(j);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* op = p.out + ((size_t)t * p.hq + h) * D + lane * E;
-    for (int e = 0; e < E; ++e) {
-        const uint32_t u = pack2<F16>(o[e] * inv, 0.f);
-        op[e] = (uint16_t)u;
-    }
-    if (p.lse && lane == 0)
-        p.lse[(size_t)h * p.T + t] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+constexpr int kPaThreads = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kPaThreads * 168, "registers of the launch");
+constexpr int kTileKeys = 128;
+constexpr int kRegion = kTileKeys * 128;     // bytes of 128 rows x 64 columns
+constexpr int kUnitCost = 1;                 // a unit's prologue and epilogue, in key tiles
+constexpr float kLazy = 8.f;
+
+// A CTA's share of a unit: key tiles [p0, p1) of its nt.
+struct Piece {
+    int tok0, ntok, g, r;
+    int pos0;           // position of the first token
+    int lo, hi;         // keys that some row sees lie in [lo, hi]
+    int tile0;          // all keys: the first key tile's number
+    int nb;             // selected blocks: entries of the list
+    int p0, p1, nt;
+    int slot;           // partial slot, or -1: the piece is the whole unit
+    int more;           // 0: no piece, the CTA is done
+};
+
+constexpr int kRing = 8;
+
+template <int D>
+struct alignas(1024) PaSmem {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    uint8_t q[2][kHalves][kRegion];           // NQ = 2: the unit's two tiles; NQ = 1: two units
+    uint8_t kv[kStages][kHalves][kRegion];    // K and V tiles in the order the issuer uses them
+    float2 xch[2][2][128];                    // NQ = 1: [unit parity][stream][row] (m, l)
+    Piece ring[kRing];                        // the scheduler's pieces, in order
+    int list[kRing][kMaxTopk];                // selected blocks: the valid ones of each
+    uint64_t ring_full[kRing], ring_empty[kRing];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2];
+    uint64_t xbar, drain;
+    long long start_x, end_x, start_off, total_cost;
+    int start_head, start_req, start_tile;
+    long long wsum[kPaThreads / 32];
+    uint32_t tmem_base;
+    int abort_flag, err;
+};
+
+struct Params {
+    PagedAttnArgs a;
+    int tpt;            // tokens per 128-row tile
+    int box_rows;       // rows of one K / V box
+    int splits;         // selected blocks: CTAs per unit
+    float* part_o;      // [pieces][NQ * 128][D]
+    float2* part_ml;    // [pieces][NQ * 128] (m, l)
+    int4* desc;         // all keys: [grid] unit left open by CTA c: (token, ntok, g, last CTA)
+};
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                            int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+// 16 consecutive fp32 columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "{\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const float* v) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+    asm volatile(
+        "{\n\t"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+        "tcgen05.wait::st.sync.aligned;\n\t}"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Request r: rows [a, a + n) of q, kv keys, all inside their buffers whatever the arrays say.
+struct Req { int a, n, kv; };
+__device__ __forceinline__ Req request(const PagedAttnArgs& p, int r) {
+    Req q;
+    q.a = min(max(__ldg(p.cu + r), 0), p.T);
+    q.n = min(max(__ldg(p.cu + r + 1), q.a), p.T) - q.a;
+    q.kv = min(max(__ldg(p.kv_lens + r), 0), p.table_width * p.ps);
+    return q;
+}
+__device__ __forceinline__ bool request_ok(const PagedAttnArgs& p, int r) {
+    const int a = __ldg(p.cu + r), b = __ldg(p.cu + r + 1), kv = __ldg(p.kv_lens + r);
+    return a >= 0 && b >= a && b <= p.T && kv >= 0 && kv <= p.table_width * p.ps;
+}
+
+// Visible keys of tokens [t, t + ntok) of a request, as [lo, hi]; key tiles touched.
+__device__ __forceinline__ void unit_keys(const Req& q, int t, int ntok, int swin, int* pos0, int* lo,
+                                          int* hi, int* nt) {
+    *pos0 = q.kv - q.n + t;
+    *hi = *pos0 + ntok - 1;                    // < kv
+    *lo = swin > 0 ? max(0, *pos0 - swin + 1) : 0;
+    *nt = *hi < 0 ? 0 : *hi / kTileKeys - *lo / kTileKeys + 1;
+}
+
+// All keys: the walk over a CTA's piece [x, x1) of the line of (KV head, request, tile of
+// tokens, key tile) with kUnitCost places more per unit.
+struct WalkAll {
+    long long x, x1, u0;
+    int head, r, qt;
+    int open;           // pieces already left open at their start (slot numbers)
+    __device__ __forceinline__ bool next(const Params& P, int tpu, int cta, Piece& k) {
+        const PagedAttnArgs& p = P.a;
+        while (x < x1) {
+            Req q = request(p, r);
+            while ((long long)qt * tpu >= q.n) {
+                qt = 0;
+                if (++r == p.R) { r = 0; ++head; }
+                q = request(p, r);
+            }
+            const int t = qt * tpu;
+            k.ntok = min(tpu, q.n - t);
+            k.tok0 = q.a + t;
+            k.g = head;
+            k.r = r;
+            unit_keys(q, t, k.ntok, p.swin, &k.pos0, &k.lo, &k.hi, &k.nt);
+            k.tile0 = k.lo / kTileKeys;
+            const long long cost = k.nt + kUnitCost, u1 = min(cost, u0 + (x1 - x));
+            const bool first = u0 == 0;
+            k.p0 = (int)min(u0, (long long)k.nt);
+            k.p1 = (int)min(u1, (long long)k.nt);
+            k.slot = k.p0 == 0 && k.p1 == k.nt ? -1 : 2 * cta + (k.p0 == 0 ? 1 : 0);
+            x += u1 - u0;
+            if (u1 == cost) { ++qt; u0 = 0; } else u0 = u1;
+            if (k.p0 < k.p1 || (k.nt == 0 && first)) return true;
+        }
+        return false;
+    }
+};
+
+// Selected blocks: items (token, KV head, split), one after another round the CTAs.
+// Called by a whole warp: the unit's valid blocks are compacted into the list.
+struct WalkSel {
+    long long item, items;
+    int r;
+    __device__ __forceinline__ bool next(const Params& P, int grid, int lane, int* list, Piece& k) {
+        const PagedAttnArgs& p = P.a;
+        const int t_first = __ldg(p.cu), t_last = __ldg(p.cu + p.R);
+        for (; item < items; item += grid) {
+            const long long u = item / P.splits;
+            const int s = (int)(item - u * P.splits);
+            const int t = (int)(u / p.hkv), g = (int)(u - (long long)t * p.hkv);
+            if (t < t_first || t >= t_last) continue;
+            r = seq_of_token(p.cu, p.R, t);
+            const Req q = request(p, r);
+            if (t < q.a || t >= q.a + q.n) continue;
+            int nt;
+            unit_keys(q, t - q.a, 1, p.swin, &k.pos0, &k.lo, &k.hi, &nt);
+            const int pos = k.pos0, qb = pos >= 0 ? pos / p.bs : -1;
+            const int32_t* row = p.bidx + u * p.topk;
+            const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
+            const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
+            const unsigned m0 = __ballot_sync(0xffffffffu, block_valid(b0, qb, pos, p.bs, p.swin));
+            const unsigned m1 = __ballot_sync(0xffffffffu, block_valid(b1, qb, pos, p.bs, p.swin));
+            const unsigned below = (1u << lane) - 1u;
+            __syncwarp();
+            if (m0 >> lane & 1) list[__popc(m0 & below)] = b0;
+            if (m1 >> lane & 1) list[__popc(m0) + __popc(m1 & below)] = b1;
+            __syncwarp();
+            k.nb = __popc(m0) + __popc(m1);
+            k.tok0 = t;
+            k.ntok = 1;
+            k.g = g;
+            k.r = r;
+            const int per = kTileKeys / p.bs;
+            k.nt = (k.nb + per - 1) / per;
+            k.p0 = (int)((long long)s * k.nt / P.splits);
+            k.p1 = (int)((long long)(s + 1) * k.nt / P.splits);
+            k.slot = P.splits > 1 ? (int)item : -1;
+            item += grid;
+            return true;
+        }
+        return false;
+    }
+};
+
+// The visible columns of key tile j of a piece, as two inclusive ranges: columns
+// [l0, h0] of the first 64 and [l1, h1] of the last 64 (empty: l > h).  For the unit as a
+// whole; rows narrow them further.
+template <bool SEL>
+__device__ __forceinline__ void tile_cols(const Params& P, const Piece& k, const int* list, int j, int& l0,
+                                          int& h0, int& l1, int& h1) {
+    if (!SEL) {
+        const int key0 = (k.tile0 + j) * kTileKeys;
+        l0 = max(k.lo - key0, 0);
+        h1 = min(k.hi - key0, 127);
+        h0 = min(h1, 63);
+        l1 = max(l0, 64);
+    } else if (P.a.bs == 128) {
+        const int key0 = list[j] * 128;
+        l0 = max(k.lo - key0, 0);
+        h1 = min(k.hi - key0, 127);
+        h0 = min(h1, 63);
+        l1 = max(l0, 64);
+    } else {
+        const int key0 = list[2 * j] * 64;
+        l0 = max(k.lo - key0, 0);
+        h0 = min(k.hi - key0, 63);
+        l1 = 128;
+        h1 = -1;
+        if (2 * j + 1 < k.nb) {
+            const int key1 = list[2 * j + 1] * 64;
+            l1 = 64 + max(k.lo - key1, 0);
+            h1 = 64 + min(k.hi - key1, 63);
+        }
+    }
+}
+
+template <int F16, int D, int NQ, bool SEL>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    k_paged_attn(const Params P, const __grid_constant__ CUtensorMap qmap,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using Smem = PaSmem<D>;
+    constexpr int kHalves = Smem::kHalves, kStages = Smem::kStages;
+    constexpr int kAhead = NQ == 2 ? 1 : 2;       // K tiles loaded and multiplied ahead of V
+    extern __shared__ uint8_t smem_raw[];
+    Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PagedAttnArgs& p = P.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
+    const int tpu = NQ * P.tpt;
+
+    if (tid == 0) {
+        S.abort_flag = 0;
+        S.err = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.q_empty[i], 1);
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.pv_done[i], 1);
+            mbar_init(&S.o_full[i], 1);
+            mbar_init(&S.o_empty[i], NQ == 2 ? 4 : 8);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&S.kv_full[i], 1);
+            mbar_init(&S.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&S.ring_full[i], 1);
+            mbar_init(&S.ring_empty[i], 10);   // producer, issuer, eight softmax warps
+        }
+        mbar_init(&S.xbar, 8);
+        mbar_init(&S.drain, 1);
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        __syncwarp();
+        tmem_alloc(&S.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (tid == 11 * 32) {
+        prefetch_tmap(&qmap);
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    __syncthreads();
+    if (SEL) {
+        for (int r = cta * kPaThreads + tid; r < p.R; r += grid * kPaThreads)
+            if (!request_ok(p, r)) S.err = NSA_ERR_BAD_INDEX;
+    } else {
+        // This CTA's piece of the line: every CTA sums the costs of all requests by itself
+        // (one thread per request, or one warp where they are few), from the lengths alone.
+        long long* pre = reinterpret_cast<long long*>(S.kv[0][0]);   // [R], before any load
+        const int group = p.R >= 192 ? 1 : 32;
+        bool bad = false;
+        for (int r = tid / group; r < p.R; r += kPaThreads / group) {
+            const Req q = request(p, r);
+            bad |= !request_ok(p, r);
+            long long cost = 0;
+            for (int t = (tid % group) * tpu; t < q.n; t += group * tpu) {
+                int pos0, lo, hi, nt;
+                unit_keys(q, t, min(tpu, q.n - t), p.swin, &pos0, &lo, &hi, &nt);
+                cost += nt + kUnitCost;
+            }
+            if (group == 32)
+                for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+            if (tid % group == 0) pre[r] = cost;
+        }
+        if (bad && cta == 0) S.err = NSA_ERR_BAD_INDEX;
+        __syncthreads();
+        const int per = (p.R + kPaThreads - 1) / kPaThreads;
+        const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+        long long mine = 0;
+        for (int r = r0; r < r1; ++r) mine += pre[r];
+        long long inc = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) S.wsum[warp] = inc;
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < kPaThreads / 32; ++w) {
+            if (w < warp) inc += S.wsum[w];
+            all += S.wsum[w];
+        }
+        const long long total = all * p.hkv;
+        const long long pieces = min((long long)grid, total);
+        const long long x0 = cta < pieces ? cta * total / pieces : 0;
+        if (tid == 0) {
+            S.start_x = x0;
+            S.end_x = cta < pieces ? (cta + 1) * total / pieces : 0;
+            S.total_cost = total;
+        }
+        if (cta < pieces) {
+            const long long rem = x0 % all;
+            long long before = inc - mine;
+            if (rem >= before && rem < inc) {         // one thread: its requests hold the start
+                int r = r0;
+                while (rem >= before + pre[r]) before += pre[r++];
+                const Req q = request(p, r);
+                long long off = rem - before;
+                int qt = 0;
+                for (;; ++qt) {
+                    int pos0, lo, hi, nt;
+                    unit_keys(q, qt * tpu, min(tpu, q.n - qt * tpu), p.swin, &pos0, &lo, &hi, &nt);
+                    if (off < nt + kUnitCost) break;
+                    off -= nt + kUnitCost;
+                }
+                S.start_head = (int)(x0 / all);
+                S.start_req = r;
+                S.start_tile = qt;
+                S.start_off = off;
+            }
+        }
+        __syncthreads();
+        // generic writes to the stages come before the TMA writes that follow
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    volatile int* abort_flag = &S.abort_flag;
+    // Bounded wait of a whole warp; false in every lane if any lane gave up.
+    auto wait_lane = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        const long long start = clock64();
+#pragma unroll 1
+        while (!mbar_try_wait(bar, parity)) {
+            if (clock64() - start > kWaitBudgetCycles) {
+                S.err = NSA_ERR_TIMEOUT;
+                *abort_flag = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_lane(bar, parity));
+    };
+    // piece i of the ring, once it is there; release(i): this warp is done with it
+    auto fetch = [&](int i) -> bool { return wait(&S.ring_full[i % kRing], (i / kRing) & 1); };
+    auto release = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.ring_empty[i % kRing]);
+    };
+
+    // setmaxnreg at the head of each role: the compiler gives the code behind it that many
+    if (warp >= 8) {
+        set_regs_dec<kOtherRegs>();
+    if (warp == 8) {
+        // ------------------------------------------------------------- TMA producer
+        const int boxes = kTileKeys / P.box_rows;      // per tile and 64-column half
+        const int box = lane / kHalves, half = lane - box * kHalves;
+        const uint32_t box_bytes = (uint32_t)P.box_rows * 128u;
+        int n = 0;                  // tiles put into the stages
+        int units = 0;              // units whose Q was loaded
+        int at = -1;                // piece being loaded
+        int j = 0, j_end = 0;       // its next key tile
+        // the tiles whose K is on its way and whose V is not
+        int page_q[kAhead] = {}, row_q[kAhead] = {}, g_q[kAhead] = {};
+        unsigned mask_q[kAhead] = {};
+        int pending = 0;
+        bool ok = true, more = true;
+        auto load = [&](const CUtensorMap* map, int page, int row, int g, unsigned mask) -> bool {
+            const int stg = n % kStages;
+            if (!wait(&S.kv_empty[stg], ((n / kStages) & 1) ^ 1)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[stg], (uint32_t)__popc(mask) * box_bytes);
+            __syncwarp();
+            if (mask >> lane & 1)
+                tma_load_4d(S.kv[stg][half] + box * box_bytes, map, &S.kv_full[stg], half * 64, g, row, page);
+            ++n;
+            return true;
+        };
+        while (ok) {
+            while (more && j == j_end) {          // the next piece with a key tile
+                if (at >= 0) release(at);
+                ++at;
+                if (!(ok = fetch(at))) break;
+                const Piece& k = S.ring[at % kRing];
+                more = k.more != 0;
+                j = k.p0;
+                j_end = k.p1;
+                if (!more || j == j_end) continue;
+                const int qb = NQ == 2 ? 0 : units & 1;
+                const int use = NQ == 2 ? units : units >> 1;
+                if (!(ok = wait(&S.q_empty[qb], (use & 1) ^ 1))) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&S.q_full[qb], (uint32_t)(NQ * kHalves * P.tpt * p.G) * 128u);
+                __syncwarp();
+                if (lane < NQ * kHalves) {
+                    const int tile = lane / kHalves, hf = lane - tile * kHalves;
+                    tma_load_3d(S.q[NQ == 2 ? tile : qb][hf], &qmap, &S.q_full[qb], hf * 64, k.g * p.G,
+                                k.tok0 + tile * P.tpt);
+                }
+                ++units;
+            }
+            if (!ok) break;
+            if (more) {
+                // this lane's box of key tile j: the page, the row in it, and whether a
+                // visible key lies in it
+                const Piece& k = S.ring[at % kRing];
+                const int c0 = box * P.box_rows;
+                int key = -1;
+                if (lane < boxes * kHalves) {
+                    if (!SEL) {
+                        key = (k.tile0 + j) * kTileKeys + c0;
+                    } else {
+                        const int e = j * (kTileKeys / p.bs) + c0 / p.bs;
+                        if (e < k.nb) key = S.list[at % kRing][e] * p.bs + c0 % p.bs;
+                    }
+                }
+                const bool live = key >= 0 && key <= k.hi && key + P.box_rows > k.lo;
+                int page = 0, row = 0;
+                if (live) {
+                    page = __ldg(p.table + (long long)k.r * p.table_stride + key / p.ps);
+                    row = key % p.ps;
+                    if (page < 0 || page >= p.num_pages) {   // reads as zeros
+                        S.err = NSA_ERR_BAD_INDEX;
+                        page = p.num_pages;
+                    }
+                }
+                const unsigned mask = __ballot_sync(0xffffffffu, live);
+                const int g = k.g;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (i == pending) {
+                        page_q[i] = page;
+                        row_q[i] = row;
+                        g_q[i] = g;
+                        mask_q[i] = mask;
+                    }
+                if (!(ok = load(&kmap, page, row, g, mask))) break;
+                ++pending;
+                ++j;
+                // the order of use: K K V K V .. V V (NQ = 1) or K V K V .. (NQ = 2)
+                if (pending < kAhead) continue;
+            }
+            if (pending == 0) break;
+            if (!(ok = load(&vmap, page_q[0], row_q[0], g_q[0], mask_q[0]))) break;
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) {
+                page_q[i] = page_q[i + 1];
+                row_q[i] = row_q[i + 1];
+                g_q[i] = g_q[i + 1];
+                mask_q[i] = mask_q[i + 1];
+            }
+            --pending;
+        }
+        if (*abort_flag && lane == 0) {   // let copies still in flight land before the CTA exits
+            const long long start = clock64();
+            auto land = [&](uint64_t* bar, uint32_t parity) {
+                while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitBudgetCycles) {}
+            };
+            for (int i = 0; i < 2; ++i) {
+                const int uses = NQ == 2 ? (i == 0 ? units : 0) : (units + 1 - i) / 2;
+                if (uses > 0) land(&S.q_full[i], (uses - 1) & 1);
+            }
+            for (int i = max(n - kStages, 0); i < n; ++i) land(&S.kv_full[i % kStages], (i / kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // -------------------------------------------------------------- MMA issuer
+        const uint32_t elected = elect_one();
+        constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
+        constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
+        constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+        const uint32_t q_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024);
+        const uint32_t k_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024);
+        const uint32_t v_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), kRegion, 1024);
+        // Two cursors over the same pieces: the products S run two items ahead of the
+        // products P V (an item: a key tile for one stream; items alternate between the
+        // streams).  S(i + 2) follows P V(i) of its stream on the in-order tensor pipe, which
+        // is what lets P share the columns of S.
+        int n = 0;                        // stages used
+        int s_items = 0, o_items = 0;     // items issued
+        int at_s = -1, at_o = -1;         // pieces
+        int js = 0, js_end = 0, jo = 0, jo_end = 0;
+        int units_s = 0;
+        int ks_stage = 0, vo_stage = 0;
+        bool ok = true, more_s = true, more_o = true;
+        int o_cnt[2] = {0, 0};            // sums each stream has completed
+        int o_first[2] = {0, 0};          // the stream's next P V starts a sum
+        auto advance_s = [&]() {          // to the piece of S(s_items)
+            while (ok && more_s && js == js_end) {
+                if (!(ok = fetch(++at_s))) return;
+                const Piece& k = S.ring[at_s % kRing];
+                more_s = k.more != 0;
+                js = k.p0;
+                js_end = k.p1;
+                if (more_s && js < js_end) ++units_s;
+            }
+        };
+        auto advance_o = [&]() {
+            while (ok && more_o && jo == jo_end) {
+                if (at_o >= 0) release(at_o);
+                if (!(ok = fetch(++at_o))) return;
+                const Piece& k = S.ring[at_o % kRing];
+                more_o = k.more != 0;
+                jo = k.p0;
+                jo_end = k.p1;
+                o_first[0] = o_first[1] = 1;
+            }
+        };
+        auto issue_s = [&]() -> bool {
+            const Piece& ks = S.ring[at_s % kRing];
+            const int st = s_items & 1;
+            const int qsub = NQ == 2 ? st : 0;
+            const int qb = NQ == 2 ? 0 : (units_s - 1) & 1;
+            if (js == ks.p0 && qsub == 0) {
+                const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
+                if (!wait(&S.q_full[qb], use & 1)) return false;
+            }
+            if (qsub == 0) {
+                ks_stage = n % kStages;
+                if (!wait(&S.kv_full[ks_stage], (n / kStages) & 1)) return false;
+                ++n;
+            }
+            tc_fence_after();
+            const uint32_t a0 = q_desc0 + (uint32_t)(NQ == 2 ? qsub : qb) * kTileU;
+            const uint32_t b0 = k_desc0 + (uint32_t)ks_stage * kTileU;
+            if (qsub == 0 || ks.ntok > P.tpt) {
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = (uint32_t)((s >> 2) * kHalfU + (s & 3) * 2);
+                    mma_ss_e(tmem + (uint32_t)st * 128u, a0 + off, b0 + off, kIdescS, s > 0 ? 1u : 0u, elected);
+                }
+            }
+            mma_commit_e(&S.s_full[st], elected);
+            if (NQ == 1 || qsub == 1) {
+                mma_commit_e(&S.kv_empty[ks_stage], elected);
+                if (js + 1 == ks.p1) mma_commit_e(&S.q_empty[qb], elected);
+                ++js;
+            }
+            ++s_items;
+            return true;
+        };
+        auto issue_pv = [&]() -> bool {
+            const Piece& ko = S.ring[at_o % kRing];
+            const int st = o_items & 1;
+            const int qsub = NQ == 2 ? st : 0;
+            int l0, h0, l1, h1;
+            tile_cols<SEL>(P, ko, S.list[at_o % kRing], jo, l0, h0, l1, h1);
+            if (qsub == 0) {
+                vo_stage = n % kStages;
+                if (!wait(&S.kv_full[vo_stage], (n / kStages) & 1)) return false;
+                ++n;
+                // clear the rows of the used 16-key steps that nobody may see
+                uint8_t* v = S.kv[vo_stage][0];
+                bool cleared = false;
+                auto clear = [&](int from, int to) {
+                    for (int r = from; r < to; ++r) {
+                        if (lane < 8 * kHalves)
+                            *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        cleared = true;
+                    }
+                };
+                if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
+                if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
+                if (cleared) fence_async_smem();
+                __syncwarp();
+            }
+            if (o_first[st]) {
+                if (o_cnt[st] > 0 && !wait(&S.o_empty[st], (o_cnt[st] - 1) & 1)) return false;
+            }
+            if (!wait(&S.p_full[st], (o_items >> 1) & 1)) return false;
+            tc_fence_after();
+            const uint32_t tP = tmem + (uint32_t)st * 128u, tO = tmem + 256u + (uint32_t)st * 128u;
+            const uint32_t b0 = v_desc0 + (uint32_t)vo_stage * kTileU;
+            if (qsub == 0 || ko.ntok > P.tpt) {
+                uint32_t acc = o_first[st] ? 0u : 1u;
+#pragma unroll
+                for (int s = 0; s < kTileKeys / 16; ++s) {
+                    const bool use = s < 4 ? (l0 <= h0 && 16 * s + 15 >= l0 && 16 * s <= h0)
+                                           : (l1 <= h1 && 16 * s + 15 >= l1 && 16 * s <= h1);
+                    if (use) {
+                        mma_ts_e(tO, tP + (uint32_t)s * 8u, b0 + (uint32_t)s * 128u, kIdescO, acc, elected);
+                        acc = 1u;
+                    }
+                }
+            }
+            o_first[st] = 0;
+            mma_commit_e(&S.pv_done[st], elected);
+            // the stream's last item of the unit: O is complete
+            if (NQ == 2 ? jo + 1 == ko.p1 : jo + 2 >= ko.p1) {
+                mma_commit_e(&S.o_full[st], elected);
+                ++o_cnt[st];
+            }
+            if (NQ == 1 || qsub == 1) {
+                mma_commit_e(&S.kv_empty[vo_stage], elected);
+                ++jo;
+            }
+            ++o_items;
+            return true;
+        };
+        for (int i = 0; i < 2 && ok; ++i) {
+            advance_s();
+            if (ok && more_s) ok = issue_s();
+        }
+        while (ok) {
+            advance_o();
+            if (!ok || !more_o) break;
+            if (!(ok = issue_pv())) break;
+            advance_s();
+            if (ok && more_s) ok = issue_s();
+        }
+        mma_commit_e(&S.drain, elected);
+        {
+            const long long start = clock64();
+            while (!mbar_try_wait(&S.drain, 0) && clock64() - start < kWaitBudgetCycles) {}
+        }
+    } else if (warp == 10) {
+        // --------------------------------------------------------------- scheduler
+        WalkAll wall{};
+        WalkSel wsel{};
+        if (SEL) {
+            wsel.item = cta;
+            wsel.items = (long long)p.T * p.hkv * P.splits;
+        } else {
+            wall.x = S.start_x;
+            wall.x1 = S.end_x;
+            wall.head = S.start_head;
+            wall.r = S.start_req;
+            wall.qt = S.start_tile;
+            wall.u0 = S.start_off;
+        }
+        // the unit this CTA starts and leaves open, for the merge, and who finishes it
+        int4 open = make_int4(0, 0, 0, -1);
+        for (int i = 0;; ++i) {
+            const int at = i % kRing;
+            if (!wait(&S.ring_empty[at], ((i / kRing) & 1) ^ 1)) break;
+            Piece k{};
+            k.more = SEL ? wsel.next(P, grid, lane, S.list[at], k) : wall.next(P, tpu, cta, k);
+            if (!SEL && k.more && k.slot == 2 * cta + 1) {
+                // line place of the unit's last key tile: the walk ended inside the unit
+                const long long total = S.total_cost, pieces = min((long long)grid, total);
+                const long long last = wall.x1 - wall.u0 + k.nt - 1;
+                open = make_int4(k.tok0, k.ntok, k.g, (int)(((last + 1) * pieces - 1) / total));
+            }
+            if (lane == 0) S.ring[at] = k;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.ring_full[at]);
+            if (!k.more) break;
+        }
+        if (!SEL && lane == 0) P.desc[cta] = open;
+    }
+    } else {
+        set_regs_inc<kSoftmaxRegs>();
+        // ------------------------------------------------------- softmax and epilogue
+        const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + lane_off + (uint32_t)st * 128u;
+        const int rt = row / p.G, head = row - rt * p.G;
+        const float c = p.scale_log2;
+        int items = 0;                    // this stream's items so far
+        int tiles = 0;                    // NQ = 1: key tiles so far, both streams
+        int units = 0;                    // units with a key tile
+        int o_cnt[2] = {0, 0};            // sums each stream has completed
+        bool ok = true;
+        for (int at = 0;; ++at) {
+            if (!(ok = fetch(at))) break;
+            const Piece& k = S.ring[at % kRing];
+            if (!k.more) break;
+            const int* list = S.list[at % kRing];
+            const int ti = NQ == 2 ? st * P.tpt + rt : rt;         // token within the unit
+            const bool valid = rt < P.tpt && ti < k.ntok;
+            const int pos = k.pos0 + ti;
+            const int row_lo = SEL ? k.lo : (p.swin > 0 ? max(0, pos - p.swin + 1) : 0);
+            const bool active = __any_sync(0xffffffffu, valid);
+            float m = -CUDART_INF_F, l = 0.f;
+            bool first = true;
+            // NQ = 1: key tiles of the piece alternate between the streams, from where the
+            // last unit left off
+            const int step = NQ == 2 ? 1 : 2;
+            const int from = NQ == 2 ? k.p0 : k.p0 + ((tiles & 1) ^ st);
+            for (int j = from; j < k.p1; j += step, ++items) {
+                if (!(ok = wait(&S.s_full[st], items & 1))) break;
+                if (active) {
+                    tc_fence_after();
+                    float s[128];
+                    tmem_ld64_sync(tS, s);
+                    tmem_ld64_sync(tS + 64, s + 64);
+                    int l0, h0, l1, h1;
+                    tile_cols<SEL>(P, k, list, j, l0, h0, l1, h1);
+                    if (!SEL) {
+                        const int key0 = (k.tile0 + j) * kTileKeys;
+                        l0 = valid ? row_lo - key0 : 0;
+                        h0 = h1 = valid ? pos - key0 : 127;
+                        l1 = l0;
+                    }
+                    if (__any_sync(0xffffffffu, l0 > 0 || h0 < 63 || l1 > 64 || h1 < 127)) {
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) {
+                            if (x < l0 || x > h0) s[x] = -CUDART_INF_F;
+                            if (x + 64 < l1 || x + 64 > h1) s[x + 64] = -CUDART_INF_F;
+                        }
+                    }
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int x = 0; x < 128; x += 8)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) mx[y] = fmax3(mx[y], s[x + 2 * y], s[x + 2 * y + 1]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    const bool grow = valid && top > m + kLazy;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float a = grow ? ex2_approx(m - top) : 1.f;   // m = -inf: 0
+                        if (grow) m = top;
+                        l *= a;
+                        if (!first) {
+                            if (!(ok = wait(&S.pv_done[st], (items - 1) & 1))) break;
+                            tc_fence_after();
+                            const uint32_t tO = tmem + lane_off + 256u + (uint32_t)st * 128u;
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 16) {
+                                float o[16];
+                                tmem_ld16_sync(tO + x, o);
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) o[y] *= a;
+                                tmem_st16_sync(tO + x, o);
+                            }
+                        }
+                    }
+                    first = false;
+                    const float mm = m == -CUDART_INF_F ? 0.f : m;
+                    const float2 c2 = make_float2(c, c), m2 = make_float2(-mm, -mm);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t pk[64];
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) {
+                        float2 e = fma2(make_float2(s[2 * x], s[2 * x + 1]), c2, m2);
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        sum[x & 1] = add2(sum[x & 1], e);
+                        pk[x] = pack2<F16>(e.x, e.y);
+                    }
+                    tmem_st32_sync(tS, pk);
+                    tmem_st32_sync(tS + 32, pk + 32);
+                    const float2 t2 = add2(sum[0], sum[1]);
+                    l += t2.x + t2.y;
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_full[st]);
+            }
+            if (!ok) break;
+            const int nt = k.p1 - k.p0;
+            const int n0 = NQ == 2 ? nt : (nt + 1 - (tiles & 1)) >> 1, n1 = NQ == 2 ? nt : nt - n0;
+            tiles += nt;
+            const uint32_t tO = tmem + lane_off + 256u;
+            if (NQ == 2) {
+                if (nt > 0) {
+                    if (!(ok = wait(&S.o_full[st], o_cnt[st] & 1))) break;
+                    ++o_cnt[st];
+                    tc_fence_after();
+                }
+            } else if (nt > 0) {
+                // both streams' (m, l) of every row
+                S.xch[units & 1][st][row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.xbar);
+                ok = wait(&S.xbar, units & 1);
+                if (ok && n0 > 0) {
+                    ok = wait(&S.o_full[0], o_cnt[0] & 1);
+                    ++o_cnt[0];
+                }
+                if (ok && n1 > 0) {
+                    ok = wait(&S.o_full[1], o_cnt[1] & 1);
+                    ++o_cnt[1];
+                }
+                if (!ok) break;
+                tc_fence_after();
+            }
+            // weights of the streams' sums
+            float w0 = 0.f, w1 = 0.f;
+            if (NQ == 1 && nt > 0) {
+                const float2 a = S.xch[units & 1][0][row], b = S.xch[units & 1][1][row];
+                m = fmaxf(a.x, b.x);
+                w0 = a.y > 0.f ? ex2_approx(a.x - m) : 0.f;
+                w1 = b.y > 0.f ? ex2_approx(b.x - m) : 0.f;
+                if (!(a.y == a.y) || !(b.y == b.y)) w0 = w1 = CUDART_NAN_F;
+                l = w0 * a.y + w1 * b.y;
+            }
+            const int tok = k.tok0 + ti, hq = k.g * p.G + head;
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
+            // NQ = 1: each warpgroup takes half of the columns; NQ = 2: each its own rows
+            constexpr int kCols = NQ == 2 ? D : D / 2;
+            const int col0 = NQ == 2 ? 0 : st * kCols;
+            if (active) {
+#pragma unroll 1
+                for (int x = 0; x < kCols; x += 16) {
+                    float o[16];
+                    if (NQ == 2) {
+                        if (nt > 0) tmem_ld16_sync(tO + (uint32_t)(st * 128 + x), o);
+                    } else {
+                        // a weight of 0 belongs to a sum that may never have been started
+                        float o1[16];
+                        tmem_ld16_sync(tO + (uint32_t)(col0 + x), o);
+                        tmem_ld16_sync(tO + (uint32_t)(128 + col0 + x), o1);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            o[y] = (w0 != 0.f ? w0 * o[y] : 0.f) + (w1 != 0.f ? w1 * o1[y] : 0.f);
+                    }
+                    if (l == 0.f) {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = 0.f;
+                    }
+                    if (!valid) continue;
+                    if (k.slot < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)tok * p.hq + hq) * D + col0 + x);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            dst[y] = make_uint4(pack2<F16>(o[8 * y] * inv, o[8 * y + 1] * inv),
+                                                pack2<F16>(o[8 * y + 2] * inv, o[8 * y + 3] * inv),
+                                                pack2<F16>(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
+                                                pack2<F16>(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(
+                            P.part_o + ((size_t)k.slot * (NQ * 128) + (NQ == 2 ? st * 128 : 0) + row) * D + col0 + x);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                }
+                if (valid && (NQ == 2 || st == 0)) {
+                    if (k.slot < 0) {
+                        if (p.lse)
+                            p.lse[(size_t)hq * p.T + tok] =
+                                l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+                    } else {
+                        P.part_ml[(size_t)k.slot * (NQ * 128) + (NQ == 2 ? st * 128 : 0) + row] = make_float2(m, l);
+                    }
+                }
+            }
+            if (nt > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (NQ == 2) {
+                        mbar_arrive(&S.o_empty[st]);
+                    } else {
+                        if (n0 > 0) mbar_arrive(&S.o_empty[0]);
+                        if (n1 > 0) mbar_arrive(&S.o_empty[1]);
+                    }
+                }
+                ++units;
+            }
+            release(at);
+        }
+    }
+
+    // ---- teardown: every role has left its loop (all waits are bounded) and the issuer
+    //      has drained its tensor-core work
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (tid == 0) {
+        // one status byte per CTA, always written: nothing has to be cleared before the call
+        p.st->cta_err[cta] = (unsigned char)S.err;
+        if (cta == 0) {
+            p.st->code = 0;
+            for (int i = grid; i < kMaxStatusCtas; ++i) p.st->cta_err[i] = 0;
+        }
+    }
+}
+
+// Joins the partial results of split units in the order of their pieces.  One warp per
+// row: lane i weighs piece i of each batch of 32, then all lanes add the pieces' columns.
+template <int F16, int D, bool SEL>
+__global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_per_piece, int units) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedAttnArgs& p = P.a;
+    const int lane = threadIdx.x & 31;
+    const int u = blockIdx.x;
+    int tok0, ntok, g, first, last, step0;
+    if (SEL) {
+        tok0 = u / p.hkv;
+        g = u - tok0 * p.hkv;
+        ntok = tok0 >= __ldg(p.cu) && tok0 < __ldg(p.cu + p.R) ? 1 : 0;
+        first = u * P.splits;
+        last = first + P.splits - 1;
+        step0 = 0;
+    } else {
+        const int4 d = P.desc[u];
+        if (d.w < 0) return;
+        tok0 = d.x;
+        ntok = d.y;
+        g = d.z;
+        first = u;
+        last = d.w;
+        step0 = 1;
+    }
+    const int np = last - first + 1;
+    // piece i of the unit: all keys: slot 1 of CTA first, then slot 0 of the CTAs after it
+    auto slot = [&](int i) -> size_t {
+        return SEL ? (size_t)(first + i) : (size_t)(2 * (first + i) + (i == 0 ? step0 : 0));
+    };
+    constexpr int kV = D / 32;
+    for (int y = blockIdx.y * 8 + (threadIdx.x >> 5); y < ntok * p.G; y += gridDim.y * 8) {
+        const int ti = y / p.G, h = y - ti * p.G;
+        const int row = (ti / P.tpt) * 128 + (ti % P.tpt) * p.G + h;
+        float m = -CUDART_INF_F;
+        for (int i = lane; i < np; i += 32) {
+            const float2 ml = P.part_ml[slot(i) * rows_per_piece + row];
+            if (ml.y != 0.f) m = fmaxf(m, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float acc[kV], l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+        for (int b = 0; b < np; b += 32) {
+            float w = 0.f;
+            if (b + lane < np) {
+                const float2 ml = P.part_ml[slot(b + lane) * rows_per_piece + row];
+                if (ml.y != 0.f) {
+                    w = ex2_approx(ml.x - m);
+                    l += w * ml.y;
+                }
+            }
+            const int n = min(32, np - b);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                if (wi == 0.f) continue;
+                const float* src = P.part_o + (slot(b + i) * rows_per_piece + row) * D + lane * kV;
+                if (kV == 4) {
+                    const float4 o = *reinterpret_cast<const float4*>(src);
+                    acc[0] += wi * o.x; acc[1] += wi * o.y; acc[kV - 2] += wi * o.z; acc[kV - 1] += wi * o.w;
+                } else {
+                    const float2 o = *reinterpret_cast<const float2*>(src);
+                    acc[0] += wi * o.x; acc[1] += wi * o.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
+        const int tok = tok0 + ti, hq = g * p.G + h;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)tok * p.hq + hq) * D + lane * kV);
+        dst[0] = pack2<F16>(acc[0] * inv, acc[1] * inv);
+        if (kV == 4) dst[1] = pack2<F16>(acc[kV - 2] * inv, acc[kV - 1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[(size_t)hq * p.T + tok] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+bool encode(CUtensorMap* map, bool f16, int rank, const void* base, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+    auto enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+               const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int F16, int D, int NQ, bool SEL>
+cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                   const CUtensorMap& vmap, cudaStream_t stream) {
+    const size_t smem = sizeof(PaSmem<D>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_paged_attn<F16, D, NQ, SEL>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k_paged_attn<F16, D, NQ, SEL><<<grid, kPaThreads, smem, stream>>>(P, qmap, kmap, vmap);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (SEL && P.splits == 1) return cudaSuccess;
+    // The merge is launched while the attention kernel still runs and waits for its end
+    // (programmatic dependent launch): its launch costs nothing then.
+    const int units = SEL ? P.a.T * P.a.hkv : grid;
+    const int rows = NQ * 128;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)units, (unsigned)std::min(NQ * 4, (P.a.G * (SEL ? 1 : NQ * P.tpt) + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_paged_merge<F16, D, SEL>, P, rows, units);
+}
+
+template <int F16, int D>
+cudaError_t dispatch(const Params& P, bool two, int grid, const CUtensorMap& q, const CUtensorMap& k,
+                     const CUtensorMap& v, cudaStream_t stream) {
+    if (P.a.bidx) return launch<F16, D, 1, true>(P, grid, q, k, v, stream);
+    return two ? launch<F16, D, 2, false>(P, grid, q, k, v, stream)
+               : launch<F16, D, 1, false>(P, grid, q, k, v, stream);
+}
+
+// Two tiles of query rows per unit where the batch has more than one tile of rows per
+// request and KV head on average.
+bool two_tiles(const PagedAttnArgs& p) { return (long long)p.T * p.G > 128ll * p.R; }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-cudaError_t launch_paged_attn(const PagedAttnArgs& p, int f16, int num_sms, cudaStream_t stream) {
-    const int grid = (int)(((long long)p.T * p.hq + 7) / 8);
-    if (p.d == 64) {
-        if (f16) k_paged_rows<1, 64><<<grid, 256, 0, stream>>>(p);
-        else k_paged_rows<0, 64><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (f16) k_paged_rows<1, 128><<<grid, 256, 0, stream>>>(p);
-        else k_paged_rows<0, 128><<<grid, 256, 0, stream>>>(p);
+size_t paged_attn_workspace(int d) {
+    // status, descriptors, and two open units of 256 rows per CTA
+    const size_t pieces = 2 * (size_t)kMaxStatusCtas;
+    return align256(sizeof(DevStatus)) + align256(kMaxStatusCtas * sizeof(int4)) +
+           align256(pieces * 256 * sizeof(float2)) + pieces * 256 * d * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cudaStream_t stream) {
+    Params P{};
+    P.a = a;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(a.st) + align256(sizeof(DevStatus));
+    const size_t pieces = 2 * (size_t)kMaxStatusCtas;
+    P.desc = reinterpret_cast<int4*>(ws);
+    ws += align256(kMaxStatusCtas * sizeof(int4));
+    P.part_ml = reinterpret_cast<float2*>(ws);
+    P.part_o = reinterpret_cast<float*>(ws + align256(pieces * 256 * sizeof(float2)));
+    const bool sel = a.bidx != nullptr;
+    P.tpt = sel ? 1 : kTileRows / a.G;
+    P.box_rows = std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys);
+    int grid = std::min(num_sms, kMaxStatusCtas);
+    P.splits = 1;
+    if (sel) {
+        const long long units = (long long)a.T * a.hkv;
+        const int tiles = (a.topk * a.bs + kTileKeys - 1) / kTileKeys;
+        if (units * 2 <= grid) P.splits = std::max(1, std::min(tiles, (int)(grid / units)));
+        grid = (int)std::min<long long>(grid, units * P.splits);
     }
-    return cudaGetLastError();
+    CUtensorMap qmap, kmap, vmap;
+    const cuuint64_t qdims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.hq, (cuuint64_t)a.T};
+    // (a dimension of one element may have any stride; the map wants one that is not 0)
+    auto stride = [&](long long elems, long long size) {
+        return (cuuint64_t)(size > 1 ? elems : a.d) * 2;
+    };
+    const cuuint64_t qstr[2] = {stride(a.q_head_stride, a.hq), stride(a.q_token_stride, a.T)};
+    const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)P.tpt};
+    const cuuint64_t kdims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.hkv, (cuuint64_t)a.ps,
+                                 (cuuint64_t)a.num_pages};
+    const cuuint64_t kstr[3] = {stride(a.head_stride, a.hkv), stride(a.token_stride, a.ps),
+                                stride(a.page_stride, a.num_pages)};
+    const cuuint32_t kbox[4] = {64, 1, (cuuint32_t)P.box_rows, 1};
+    if (!encode(&qmap, f16, 3, a.q, qdims, qstr, qbox) || !encode(&kmap, f16, 4, a.k, kdims, kstr, kbox) ||
+        !encode(&vmap, f16, 4, a.v, kdims, kstr, kbox))
+        return cudaErrorInvalidValue;
+    const bool two = !sel && two_tiles(a);
+    if (a.d == 64)
+        return f16 ? dispatch<1, 64>(P, two, grid, qmap, kmap, vmap, stream)
+                   : dispatch<0, 64>(P, two, grid, qmap, kmap, vmap, stream);
+    return f16 ? dispatch<1, 128>(P, two, grid, qmap, kmap, vmap, stream)
+               : dispatch<0, 128>(P, two, grid, qmap, kmap, vmap, stream);
 }
 
 }  // namespace nsa
