@@ -133,6 +133,9 @@ __device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const float* v) {
         : "memory");
 }
 
+template <int I>
+struct Stream { static constexpr int value = I; };
+
 // Request r: rows [a, a + n) of q, kv keys, all inside their buffers whatever the arrays say.
 struct Req { int a, n, kv; };
 __device__ __forceinline__ Req request(const PagedAttnArgs& p, int r) {
@@ -539,34 +542,44 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         __syncwarp();
     } else if (warp == 9) {
         // -------------------------------------------------------------- MMA issuer
-        const uint32_t elected = elect_one();
-        constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
-        constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
-        constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
-        const uint32_t q_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024);
-        const uint32_t k_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024);
-        const uint32_t v_desc0 = (uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), kRegion, 1024);
         // Two cursors over the same pieces: the products S run two items ahead of the
         // products P V (an item: a key tile for one stream; items alternate between the
         // streams).  S(i + 2) follows P V(i) of its stream on the in-order tensor pipe, which
         // is what lets P share the columns of S.
+        // The 16 MMAs of an item are 1024 cycles of tensor work, so their issue has to stay
+        // well below that: addresses that every lane holds go through u(), which lets the
+        // compiler keep them and all offsets in uniform registers, the stream is a constant of
+        // the unrolled loop, and a piece's fields are read once.
+        const uint32_t elected = elect_one();
+        constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
+        constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
+        constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+        auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+        const uint32_t tm = u(tmem);
+        const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
+        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024));
+        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), kRegion, 1024));
         int n = 0;                        // stages used
-        int s_items = 0, o_items = 0;     // items issued
         int at_s = -1, at_o = -1;         // pieces
         int js = 0, js_end = 0, jo = 0, jo_end = 0;
+        bool two_s = true, two_o = true;  // NQ = 2: the unit has rows in its second tile
+        bool head_s = false;              // S: the next item is the unit's first
+        int lo_o = 0, hi_o = 0, tile0_o = 0;
         int units_s = 0;
         int ks_stage = 0, vo_stage = 0;
         bool ok = true, more_s = true, more_o = true;
         int o_cnt[2] = {0, 0};            // sums each stream has completed
-        int o_first[2] = {0, 0};          // the stream's next P V starts a sum
-        auto advance_s = [&]() {          // to the piece of S(s_items)
+        bool o_first[2] = {true, true};   // the stream's next P V starts a sum
+        int pv_cnt = 0;                   // P V items of a stream, before this pair
+        auto advance_s = [&]() {          // to the piece of the next S
             while (ok && more_s && js == js_end) {
                 if (!(ok = fetch(++at_s))) return;
                 const Piece& k = S.ring[at_s % kRing];
                 more_s = k.more != 0;
                 js = k.p0;
                 js_end = k.p1;
-                if (more_s && js < js_end) ++units_s;
+                two_s = NQ == 2 && k.ntok > P.tpt;
+                if (more_s && js < js_end) { ++units_s; head_s = true; }
             }
         };
         auto advance_o = [&]() {
@@ -577,17 +590,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 more_o = k.more != 0;
                 jo = k.p0;
                 jo_end = k.p1;
-                o_first[0] = o_first[1] = 1;
+                two_o = NQ == 2 && k.ntok > P.tpt;
+                lo_o = k.lo;
+                hi_o = k.hi;
+                tile0_o = k.tile0;
+                o_first[0] = o_first[1] = true;
             }
         };
-        auto issue_s = [&]() -> bool {
-            const Piece& ks = S.ring[at_s % kRing];
-            const int st = s_items & 1;
-            const int qsub = NQ == 2 ? st : 0;
+        auto issue_s = [&](auto stream) -> bool {
+            constexpr int st = decltype(stream)::value;
+            constexpr int qsub = NQ == 2 ? st : 0;
             const int qb = NQ == 2 ? 0 : (units_s - 1) & 1;
-            if (js == ks.p0 && qsub == 0) {
+            if (head_s && qsub == 0) {
                 const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
                 if (!wait(&S.q_full[qb], use & 1)) return false;
+                head_s = false;
             }
             if (qsub == 0) {
                 ks_stage = n % kStages;
@@ -595,73 +612,83 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 ++n;
             }
             tc_fence_after();
-            const uint32_t a0 = q_desc0 + (uint32_t)(NQ == 2 ? qsub : qb) * kTileU;
-            const uint32_t b0 = k_desc0 + (uint32_t)ks_stage * kTileU;
-            if (qsub == 0 || ks.ntok > P.tpt) {
+            if (qsub == 0 || two_s) {
+                const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? qsub : qb) * kTileU);
+                const uint32_t b0 = u(k_desc0 + (uint32_t)ks_stage * kTileU);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (uint32_t)((s >> 2) * kHalfU + (s & 3) * 2);
-                    mma_ss_e(tmem + (uint32_t)st * 128u, a0 + off, b0 + off, kIdescS, s > 0 ? 1u : 0u, elected);
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2);
+                    mma_ss_e(tm + st * 128u, a0 + off, b0 + off, kIdescS, x > 0 ? 1u : 0u, elected);
                 }
             }
             mma_commit_e(&S.s_full[st], elected);
             if (NQ == 1 || qsub == 1) {
                 mma_commit_e(&S.kv_empty[ks_stage], elected);
-                if (js + 1 == ks.p1) mma_commit_e(&S.q_empty[qb], elected);
                 ++js;
+                if (js == js_end) mma_commit_e(&S.q_empty[qb], elected);
             }
-            ++s_items;
             return true;
         };
-        auto issue_pv = [&]() -> bool {
-            const Piece& ko = S.ring[at_o % kRing];
-            const int st = o_items & 1;
-            const int qsub = NQ == 2 ? st : 0;
-            int l0, h0, l1, h1;
-            tile_cols<SEL>(P, ko, S.list[at_o % kRing], jo, l0, h0, l1, h1);
+        auto issue_pv = [&](auto stream) -> bool {
+            constexpr int st = decltype(stream)::value;
+            constexpr int qsub = NQ == 2 ? st : 0;
+            // the tile's visible columns; all of them but at a piece's ends
+            int l0 = 0, h0 = 63, l1 = 64, h1 = 127;
+            if (SEL) {
+                tile_cols<SEL>(P, S.ring[at_o % kRing], S.list[at_o % kRing], jo, l0, h0, l1, h1);
+            } else {
+                const int key0 = (tile0_o + jo) * kTileKeys;
+                l0 = max(lo_o - key0, 0);
+                h1 = min(hi_o - key0, 127);
+                h0 = min(h1, 63);
+                l1 = max(l0, 64);
+            }
+            const bool full = l0 == 0 && h0 == 63 && l1 == 64 && h1 == 127;
             if (qsub == 0) {
                 vo_stage = n % kStages;
                 if (!wait(&S.kv_full[vo_stage], (n / kStages) & 1)) return false;
                 ++n;
-                // clear the rows of the used 16-key steps that nobody may see
-                uint8_t* v = S.kv[vo_stage][0];
-                bool cleared = false;
-                auto clear = [&](int from, int to) {
-                    for (int r = from; r < to; ++r) {
-                        if (lane < 8 * kHalves)
-                            *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        cleared = true;
-                    }
-                };
-                if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
-                if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
-                if (cleared) fence_async_smem();
-                __syncwarp();
+                if (!full) {   // clear the rows of the used 16-key steps that nobody may see
+                    uint8_t* v = S.kv[vo_stage][0];
+                    auto clear = [&](int from, int to) {
+                        for (int r = from; r < to; ++r)
+                            if (lane < 8 * kHalves)
+                                *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    };
+                    if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
+                    if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
+                    fence_async_smem();
+                    __syncwarp();
+                }
             }
-            if (o_first[st]) {
-                if (o_cnt[st] > 0 && !wait(&S.o_empty[st], (o_cnt[st] - 1) & 1)) return false;
-            }
-            if (!wait(&S.p_full[st], (o_items >> 1) & 1)) return false;
+            if (o_first[st] && o_cnt[st] > 0 && !wait(&S.o_empty[st], (o_cnt[st] - 1) & 1)) return false;
+            if (!wait(&S.p_full[st], pv_cnt & 1)) return false;
             tc_fence_after();
-            const uint32_t tP = tmem + (uint32_t)st * 128u, tO = tmem + 256u + (uint32_t)st * 128u;
-            const uint32_t b0 = v_desc0 + (uint32_t)vo_stage * kTileU;
-            if (qsub == 0 || ko.ntok > P.tpt) {
+            if (qsub == 0 || two_o) {
+                const uint32_t b0 = u(v_desc0 + (uint32_t)vo_stage * kTileU);
+                const uint32_t tP = tm + st * 128u, tO = tm + 256u + st * 128u;
                 uint32_t acc = o_first[st] ? 0u : 1u;
+                if (full) {
 #pragma unroll
-                for (int s = 0; s < kTileKeys / 16; ++s) {
-                    const bool use = s < 4 ? (l0 <= h0 && 16 * s + 15 >= l0 && 16 * s <= h0)
-                                           : (l1 <= h1 && 16 * s + 15 >= l1 && 16 * s <= h1);
-                    if (use) {
-                        mma_ts_e(tO, tP + (uint32_t)s * 8u, b0 + (uint32_t)s * 128u, kIdescO, acc, elected);
-                        acc = 1u;
+                    for (int x = 0; x < kTileKeys / 16; ++x)
+                        mma_ts_e(tO, tP + x * 8u, b0 + x * 128u, kIdescO, x == 0 ? acc : 1u, elected);
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < kTileKeys / 16; ++x) {
+                        const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
+                                               : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
+                        if (use) {
+                            mma_ts_e(tO, tP + x * 8u, b0 + x * 128u, kIdescO, acc, elected);
+                            acc = 1u;
+                        }
                     }
                 }
             }
-            o_first[st] = 0;
+            o_first[st] = false;
             mma_commit_e(&S.pv_done[st], elected);
             // the stream's last item of the unit: O is complete
-            if (NQ == 2 ? jo + 1 == ko.p1 : jo + 2 >= ko.p1) {
+            if (NQ == 2 ? jo + 1 == jo_end : jo + 2 >= jo_end) {
                 mma_commit_e(&S.o_full[st], elected);
                 ++o_cnt[st];
             }
@@ -669,19 +696,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 mma_commit_e(&S.kv_empty[vo_stage], elected);
                 ++jo;
             }
-            ++o_items;
             return true;
         };
-        for (int i = 0; i < 2 && ok; ++i) {
-            advance_s();
-            if (ok && more_s) ok = issue_s();
-        }
+        advance_s();
+        if (ok && more_s) ok = issue_s(Stream<0>{});
+        advance_s();
+        if (ok && more_s) ok = issue_s(Stream<1>{});
         while (ok) {
             advance_o();
             if (!ok || !more_o) break;
-            if (!(ok = issue_pv())) break;
+            if (!(ok = issue_pv(Stream<0>{}))) break;
             advance_s();
-            if (ok && more_s) ok = issue_s();
+            if (ok && more_s) ok = issue_s(Stream<0>{});
+            advance_o();
+            if (!ok || !more_o) break;
+            if (!(ok = issue_pv(Stream<1>{}))) break;
+            advance_s();
+            if (ok && more_s) ok = issue_s(Stream<1>{});
+            ++pv_cnt;
         }
         mma_commit_e(&S.drain, elected);
         {
