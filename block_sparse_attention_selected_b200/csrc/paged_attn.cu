@@ -14,8 +14,10 @@
 //                    one equal piece per CTA (one CTA per SM), whatever the lengths are; a
 //                    unit cut by a piece's end leaves fp32 partial results that
 //                    k_paged_merge joins in a fixed order.
-//   selected blocks  a unit is one token and walks the list of its valid blocks; units go
-//                    round the CTAs, and with fewer units than SMs each is split.
+//   selected blocks  a unit is one token and walks the list of its valid blocks.  Units go
+//                    round the CTAs, all tokens of a KV head before the next head, so that
+//                    the tokens of a chunk find the head's blocks in L2; the units that do
+//                    not fill a last round form a line as above.
 // Two streams of (S, P, O) alternate on the tensor pipe, so that one stream's softmax runs
 // under the other's products:
 //   NQ = 2  two tiles of 128 query rows over the same key tiles (long chunks);
@@ -35,6 +37,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "nsa_common.cuh"
 #include "nsa_kernels.h"
@@ -78,9 +81,6 @@ struct alignas(1024) PaSmem {
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2];
     uint64_t xbar, drain;
-    long long start_x, end_x, start_off, total_cost;
-    int start_head, start_req, start_tile;
-    long long wsum[kPaThreads / 32];
     uint32_t tmem_base;
     int abort_flag, err;
 };
@@ -89,10 +89,10 @@ struct Params {
     PagedAttnArgs a;
     int tpt;            // tokens per 128-row tile
     int box_rows;       // rows of one K / V box
-    int splits;         // selected blocks: CTAs per unit
+    int cost_sel;       // selected blocks: places of a unit on the line
     float* part_o;      // [pieces][NQ * 128][D]
     float2* part_ml;    // [pieces][NQ * 128] (m, l)
-    int4* desc;         // all keys: [grid] unit left open by CTA c: (token, ntok, g, last CTA)
+    int4* desc;         // [grid] unit left open by CTA c: (token, ntok, g, last CTA) or last = -1
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
@@ -159,12 +159,118 @@ __device__ __forceinline__ void unit_keys(const Req& q, int t, int ntok, int swi
     *nt = *hi < 0 ? 0 : *hi / kTileKeys - *lo / kTileKeys + 1;
 }
 
-// All keys: the walk over a CTA's piece [x, x1) of the line of (KV head, request, tile of
-// tokens, key tile) with kUnitCost places more per unit.
+// A line of `total` places cut into `pieces` equal parts: the part that holds place x.
+__device__ __forceinline__ int owner_of(long long x, long long total, long long pieces) {
+    return (int)(((x + 1) * pieces - 1) / total);
+}
+
+// A unit's piece [u0, u1) of its nt + kUnitCost places (the last ones hold no key tile) as
+// key tiles.  False if it holds none and nothing is to be written for it.
+__device__ __forceinline__ bool piece_tiles(long long u0, long long u1, int cta, Piece& k) {
+    k.p0 = (int)min(u0, (long long)k.nt);
+    k.p1 = (int)min(u1, (long long)k.nt);
+    k.slot = k.p0 == 0 && k.p1 == k.nt ? -1 : 2 * cta + (k.p0 == 0 ? 1 : 0);
+    k.more = 1;
+    return k.p0 < k.p1 || (k.nt == 0 && u0 == 0);
+}
+
+// All keys: a CTA's piece [x, x1) of the line of (KV head, request, tile of tokens, key
+// tile).  Run by one warp.  start(): every CTA sums the costs of all requests by itself,
+// lanes over requests (over the tiles of tokens of a long one), from the lengths alone.
 struct WalkAll {
-    long long x, x1, u0;
+    long long x, x1, u0, total, pieces;
+    long long unit_at;    // place of the piece's unit on the line
     int head, r, qt;
-    int open;           // pieces already left open at their start (slot numbers)
+    __device__ __forceinline__ static int tile_cost(const PagedAttnArgs& p, const Req& q, int i, int tpu) {
+        int pos0, lo, hi, nt;
+        unit_keys(q, i * tpu, min(tpu, q.n - i * tpu), p.swin, &pos0, &lo, &hi, &nt);
+        return nt + kUnitCost;
+    }
+    __device__ __forceinline__ static long long scan(long long v, int lane) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    }
+    // every lane's own request
+    __device__ __forceinline__ static long long cost(const PagedAttnArgs& p, const Req& q, int tpu, int lane) {
+        const int tiles = (q.n + tpu - 1) / tpu;
+        long long c = 0;
+        if (tiles <= 2)
+            for (int i = 0; i < tiles; ++i) c += tile_cost(p, q, i, tpu);
+        for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+            const int src = __ffs(many) - 1;
+            const Req h{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.kv, src)};
+            long long sum = 0;
+            for (int i = lane; i < (h.n + tpu - 1) / tpu; i += 32) sum += tile_cost(p, h, i, tpu);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == src) c = sum;
+        }
+        return c;
+    }
+    // false: the lengths are not sound
+    __device__ __forceinline__ bool start(const Params& P, int tpu, int cta, int grid, int lane) {
+        const PagedAttnArgs& p = P.a;
+        const int per = (p.R + 31) / 32;
+        long long mine = 0;
+        bool good = true;
+        auto load = [&](int i, int end) {
+            Req q{0, 0, 0};
+            if (i < end) q = request(p, i);
+            return q;
+        };
+        for (int s = 0; s < per; ++s) {
+            const int i = lane * per + s;
+            const Req q = load(i, p.R);
+            if (i < p.R) good &= request_ok(p, i);
+            mine += cost(p, q, tpu, lane);
+        }
+        const long long inc = scan(mine, lane);
+        const long long all = __shfl_sync(0xffffffffu, inc, 31);
+        total = all * p.hkv;
+        pieces = min((long long)grid, total);
+        x = x1 = u0 = 0;
+        head = r = qt = 0;
+        good = __all_sync(0xffffffffu, good);
+        if (cta >= pieces) return good;
+        x = cta * total / pieces;
+        x1 = (cta + 1) * total / pieces;
+        head = (int)(x / all);
+        long long off = x - head * all;      // in the head's part of the line
+        const unsigned holds = __ballot_sync(0xffffffffu, off < inc);
+        const int owner = __ffs(holds) - 1;
+        off -= __shfl_sync(0xffffffffu, inc - mine, owner);
+        const int end = min(p.R, (owner + 1) * per);
+        for (int base = owner * per;; base += 32) {          // the request
+            const long long c = cost(p, load(base + lane, end), tpu, lane), ci = scan(c, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                off -= __shfl_sync(0xffffffffu, ci - c, l);
+                r = base + l;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, ci, 31);
+        }
+        const Req q = request(p, r);
+        for (int base = 0;; base += 32) {                    // its tile of tokens
+            const int i = base + lane;
+            const long long c = i * tpu < q.n ? tile_cost(p, q, i, tpu) : 0, ci = scan(c, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                off -= __shfl_sync(0xffffffffu, ci - c, l);
+                qt = base + l;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, ci, 31);
+        }
+        u0 = off;
+        return good;
+    }
     __device__ __forceinline__ bool next(const Params& P, int tpu, int cta, Piece& k) {
         const PagedAttnArgs& p = P.a;
         while (x < x1) {
@@ -181,45 +287,62 @@ struct WalkAll {
             k.r = r;
             unit_keys(q, t, k.ntok, p.swin, &k.pos0, &k.lo, &k.hi, &k.nt);
             k.tile0 = k.lo / kTileKeys;
-            const long long cost = k.nt + kUnitCost, u1 = min(cost, u0 + (x1 - x));
-            const bool first = u0 == 0;
-            k.p0 = (int)min(u0, (long long)k.nt);
-            k.p1 = (int)min(u1, (long long)k.nt);
-            k.slot = k.p0 == 0 && k.p1 == k.nt ? -1 : 2 * cta + (k.p0 == 0 ? 1 : 0);
+            const long long cost = k.nt + kUnitCost, from = u0, u1 = min(cost, u0 + (x1 - x));
+            unit_at = x - u0;
             x += u1 - u0;
             if (u1 == cost) { ++qt; u0 = 0; } else u0 = u1;
-            if (k.p0 < k.p1 || (k.nt == 0 && first)) return true;
+            if (piece_tiles(from, u1, cta, k)) return true;
         }
         return false;
     }
 };
 
-// Selected blocks: items (token, KV head, split), one after another round the CTAs.
-// Called by a whole warp: the unit's valid blocks are compacted into the list.
+// Selected blocks: whole units (KV head, token) round the CTAs, then the piece [x, x1) of
+// the line of the units left over.  Run by one warp, which compacts a unit's valid blocks
+// into the list.
 struct WalkSel {
-    long long item, items;
-    int r;
-    __device__ __forceinline__ bool next(const Params& P, int grid, int lane, int* list, Piece& k) {
+    long long unit, rounds_end, x, x1, total, pieces, unit_at;
+    __device__ __forceinline__ void start(const Params& P, int cta, int grid) {
+        const long long units = (long long)P.a.T * P.a.hkv;
+        unit = cta;
+        rounds_end = units - units % grid;
+        total = (units - rounds_end) * P.cost_sel;
+        pieces = min((long long)grid, total);
+        x = cta < pieces ? cta * total / pieces : 0;
+        x1 = cta < pieces ? (cta + 1) * total / pieces : 0;
+    }
+    __device__ __forceinline__ bool next(const Params& P, int cta, int grid, int lane, int* list, Piece& k) {
         const PagedAttnArgs& p = P.a;
         const int t_first = __ldg(p.cu), t_last = __ldg(p.cu + p.R);
-        for (; item < items; item += grid) {
-            const long long u = item / P.splits;
-            const int s = (int)(item - u * P.splits);
-            const int t = (int)(u / p.hkv), g = (int)(u - (long long)t * p.hkv);
+        for (;;) {
+            long long u, u0 = 0, u1 = P.cost_sel;
+            if (unit < rounds_end) {
+                u = unit;
+                unit += grid;
+            } else if (x < x1) {
+                const long long i = x / P.cost_sel;
+                u0 = x - i * P.cost_sel;
+                u1 = min(u1, u0 + (x1 - x));
+                u = rounds_end + i;
+                unit_at = x - u0;
+                x += u1 - u0;
+            } else {
+                return false;
+            }
+            const int g = (int)(u / p.T), t = (int)(u - (long long)g * p.T);
             if (t < t_first || t >= t_last) continue;
-            r = seq_of_token(p.cu, p.R, t);
-            const Req q = request(p, r);
+            const int32_t* row = p.bidx + ((long long)t * p.hkv + g) * p.topk;
+            const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
+            const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
+            k.r = seq_of_token(p.cu, p.R, t);
+            const Req q = request(p, k.r);
             if (t < q.a || t >= q.a + q.n) continue;
             int nt;
             unit_keys(q, t - q.a, 1, p.swin, &k.pos0, &k.lo, &k.hi, &nt);
             const int pos = k.pos0, qb = pos >= 0 ? pos / p.bs : -1;
-            const int32_t* row = p.bidx + u * p.topk;
-            const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
-            const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
             const unsigned m0 = __ballot_sync(0xffffffffu, block_valid(b0, qb, pos, p.bs, p.swin));
             const unsigned m1 = __ballot_sync(0xffffffffu, block_valid(b1, qb, pos, p.bs, p.swin));
             const unsigned below = (1u << lane) - 1u;
-            __syncwarp();
             if (m0 >> lane & 1) list[__popc(m0 & below)] = b0;
             if (m1 >> lane & 1) list[__popc(m0) + __popc(m1 & below)] = b1;
             __syncwarp();
@@ -227,16 +350,10 @@ struct WalkSel {
             k.tok0 = t;
             k.ntok = 1;
             k.g = g;
-            k.r = r;
             const int per = kTileKeys / p.bs;
             k.nt = (k.nb + per - 1) / per;
-            k.p0 = (int)((long long)s * k.nt / P.splits);
-            k.p1 = (int)((long long)(s + 1) * k.nt / P.splits);
-            k.slot = P.splits > 1 ? (int)item : -1;
-            item += grid;
-            return true;
+            if (piece_tiles(u0, u1, cta, k)) return true;
         }
-        return false;
     }
 };
 
@@ -322,80 +439,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    __syncthreads();
-    if (SEL) {
-        for (int r = cta * kPaThreads + tid; r < p.R; r += grid * kPaThreads)
-            if (!request_ok(p, r)) S.err = NSA_ERR_BAD_INDEX;
-    } else {
-        // This CTA's piece of the line: every CTA sums the costs of all requests by itself
-        // (one thread per request, or one warp where they are few), from the lengths alone.
-        long long* pre = reinterpret_cast<long long*>(S.kv[0][0]);   // [R], before any load
-        const int group = p.R >= 192 ? 1 : 32;
-        bool bad = false;
-        for (int r = tid / group; r < p.R; r += kPaThreads / group) {
-            const Req q = request(p, r);
-            bad |= !request_ok(p, r);
-            long long cost = 0;
-            for (int t = (tid % group) * tpu; t < q.n; t += group * tpu) {
-                int pos0, lo, hi, nt;
-                unit_keys(q, t, min(tpu, q.n - t), p.swin, &pos0, &lo, &hi, &nt);
-                cost += nt + kUnitCost;
-            }
-            if (group == 32)
-                for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-            if (tid % group == 0) pre[r] = cost;
-        }
-        if (bad && cta == 0) S.err = NSA_ERR_BAD_INDEX;
-        __syncthreads();
-        const int per = (p.R + kPaThreads - 1) / kPaThreads;
-        const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
-        long long mine = 0;
-        for (int r = r0; r < r1; ++r) mine += pre[r];
-        long long inc = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) S.wsum[warp] = inc;
-        __syncthreads();
-        long long all = 0;
-        for (int w = 0; w < kPaThreads / 32; ++w) {
-            if (w < warp) inc += S.wsum[w];
-            all += S.wsum[w];
-        }
-        const long long total = all * p.hkv;
-        const long long pieces = min((long long)grid, total);
-        const long long x0 = cta < pieces ? cta * total / pieces : 0;
-        if (tid == 0) {
-            S.start_x = x0;
-            S.end_x = cta < pieces ? (cta + 1) * total / pieces : 0;
-            S.total_cost = total;
-        }
-        if (cta < pieces) {
-            const long long rem = x0 % all;
-            long long before = inc - mine;
-            if (rem >= before && rem < inc) {         // one thread: its requests hold the start
-                int r = r0;
-                while (rem >= before + pre[r]) before += pre[r++];
-                const Req q = request(p, r);
-                long long off = rem - before;
-                int qt = 0;
-                for (;; ++qt) {
-                    int pos0, lo, hi, nt;
-                    unit_keys(q, qt * tpu, min(tpu, q.n - qt * tpu), p.swin, &pos0, &lo, &hi, &nt);
-                    if (off < nt + kUnitCost) break;
-                    off -= nt + kUnitCost;
-                }
-                S.start_head = (int)(x0 / all);
-                S.start_req = r;
-                S.start_tile = qt;
-                S.start_off = off;
-            }
-        }
-        __syncthreads();
-        // generic writes to the stages come before the TMA writes that follow
-        fence_async_smem();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -725,15 +768,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         WalkAll wall{};
         WalkSel wsel{};
         if (SEL) {
-            wsel.item = cta;
-            wsel.items = (long long)p.T * p.hkv * P.splits;
-        } else {
-            wall.x = S.start_x;
-            wall.x1 = S.end_x;
-            wall.head = S.start_head;
-            wall.r = S.start_req;
-            wall.qt = S.start_tile;
-            wall.u0 = S.start_off;
+            wsel.start(P, cta, grid);
+            bool good = true;
+            if (cta == 0)
+                for (int r = lane; r < p.R; r += 32) good &= request_ok(p, r);
+            if (!good) S.err = NSA_ERR_BAD_INDEX;
+        } else if (!wall.start(P, tpu, cta, grid, lane)) {
+            S.err = NSA_ERR_BAD_INDEX;
         }
         // the unit this CTA starts and leaves open, for the merge, and who finishes it
         int4 open = make_int4(0, 0, 0, -1);
@@ -741,19 +782,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const int at = i % kRing;
             if (!wait(&S.ring_empty[at], ((i / kRing) & 1) ^ 1)) break;
             Piece k{};
-            k.more = SEL ? wsel.next(P, grid, lane, S.list[at], k) : wall.next(P, tpu, cta, k);
-            if (!SEL && k.more && k.slot == 2 * cta + 1) {
-                // line place of the unit's last key tile: the walk ended inside the unit
-                const long long total = S.total_cost, pieces = min((long long)grid, total);
-                const long long last = wall.x1 - wall.u0 + k.nt - 1;
-                open = make_int4(k.tok0, k.ntok, k.g, (int)(((last + 1) * pieces - 1) / total));
+            if (SEL) {
+                if (!wsel.next(P, cta, grid, lane, S.list[at], k)) k.more = 0;
+            } else {
+                if (!wall.next(P, tpu, cta, k)) k.more = 0;
             }
+            if (k.more && k.slot == 2 * cta + 1)     // its last key tile's place on the line
+                open = make_int4(k.tok0, k.ntok, k.g,
+                                 SEL ? owner_of(wsel.unit_at + k.nt - 1, wsel.total, wsel.pieces)
+                                     : owner_of(wall.unit_at + k.nt - 1, wall.total, wall.pieces));
             if (lane == 0) S.ring[at] = k;
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.ring_full[at]);
             if (!k.more) break;
         }
-        if (!SEL && lane == 0) P.desc[cta] = open;
+        if (lane == 0) P.desc[cta] = open;
     }
     } else {
         set_regs_inc<kSoftmaxRegs>();
@@ -975,82 +1018,66 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
 }
 
-// Joins the partial results of split units in the order of their pieces.  One warp per
-// row: lane i weighs piece i of each batch of 32, then all lanes add the pieces' columns.
-template <int F16, int D, bool SEL>
-__global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_per_piece, int units) {
+// Joins the partial results of the unit that CTA blockIdx.x left open, in the order of the
+// pieces.  One warp per row: lane i weighs piece i of each batch of 32, then all lanes add
+// the pieces' columns, eight pieces' loads in flight.
+template <int F16, int D>
+__global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_per_piece) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedAttnArgs& p = P.a;
-    const int lane = threadIdx.x & 31;
-    const int u = blockIdx.x;
-    int tok0, ntok, g, first, last, step0;
-    if (SEL) {
-        tok0 = u / p.hkv;
-        g = u - tok0 * p.hkv;
-        ntok = tok0 >= __ldg(p.cu) && tok0 < __ldg(p.cu + p.R) ? 1 : 0;
-        first = u * P.splits;
-        last = first + P.splits - 1;
-        step0 = 0;
-    } else {
-        const int4 d = P.desc[u];
-        if (d.w < 0) return;
-        tok0 = d.x;
-        ntok = d.y;
-        g = d.z;
-        first = u;
-        last = d.w;
-        step0 = 1;
-    }
-    const int np = last - first + 1;
-    // piece i of the unit: all keys: slot 1 of CTA first, then slot 0 of the CTAs after it
-    auto slot = [&](int i) -> size_t {
-        return SEL ? (size_t)(first + i) : (size_t)(2 * (first + i) + (i == 0 ? step0 : 0));
+    const int4 d = P.desc[blockIdx.x];
+    if (d.w < 0) return;
+    const int lane = threadIdx.x & 31, first = blockIdx.x, np = d.w - first + 1;
+    // piece 0 lies in slot 1 of CTA first, piece i in slot 0 of CTA first + i
+    auto at = [&](int i, int row) -> size_t {
+        return (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * rows_per_piece + row;
     };
     constexpr int kV = D / 32;
-    for (int y = blockIdx.y * 8 + (threadIdx.x >> 5); y < ntok * p.G; y += gridDim.y * 8) {
+    using Vec = typename std::conditional<kV == 4, float4, float2>::type;
+    for (int y = blockIdx.y * 8 + (threadIdx.x >> 5); y < d.y * p.G; y += gridDim.y * 8) {
         const int ti = y / p.G, h = y - ti * p.G;
         const int row = (ti / P.tpt) * 128 + (ti % P.tpt) * p.G + h;
         float m = -CUDART_INF_F;
         for (int i = lane; i < np; i += 32) {
-            const float2 ml = P.part_ml[slot(i) * rows_per_piece + row];
+            const float2 ml = P.part_ml[at(i, row)];
             if (ml.y != 0.f) m = fmaxf(m, ml.x);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float acc[kV], l = 0.f;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+        float acc[kV] = {}, l = 0.f;
         for (int b = 0; b < np; b += 32) {
             float w = 0.f;
             if (b + lane < np) {
-                const float2 ml = P.part_ml[slot(b + lane) * rows_per_piece + row];
+                const float2 ml = P.part_ml[at(b + lane, row)];
                 if (ml.y != 0.f) {
                     w = ex2_approx(ml.x - m);
                     l += w * ml.y;
                 }
             }
             const int n = min(32, np - b);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                if (wi == 0.f) continue;
-                const float* src = P.part_o + (slot(b + i) * rows_per_piece + row) * D + lane * kV;
-                if (kV == 4) {
-                    const float4 o = *reinterpret_cast<const float4*>(src);
-                    acc[0] += wi * o.x; acc[1] += wi * o.y; acc[kV - 2] += wi * o.z; acc[kV - 1] += wi * o.w;
-                } else {
-                    const float2 o = *reinterpret_cast<const float2*>(src);
-                    acc[0] += wi * o.x; acc[1] += wi * o.y;
+            for (int c = 0; c < n; c += 8) {
+                Vec o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = *reinterpret_cast<const Vec*>(P.part_o + at(b + min(c + i, n - 1), row) * D + lane * kV);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, w, (c + i) & 31);
+                    if (c + i < n) {
+                        const float* e = reinterpret_cast<const float*>(&o[i]);
+#pragma unroll
+                        for (int x = 0; x < kV; ++x) acc[x] += wi * e[x];
+                    }
                 }
             }
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
-        const int tok = tok0 + ti, hq = g * p.G + h;
+        const int tok = d.x + ti, hq = d.z * p.G + h;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)tok * p.hq + hq) * D + lane * kV);
-        dst[0] = pack2<F16>(acc[0] * inv, acc[1] * inv);
-        if (kV == 4) dst[1] = pack2<F16>(acc[kV - 2] * inv, acc[kV - 1] * inv);
+#pragma unroll
+        for (int x = 0; x < kV / 2; ++x) dst[x] = pack2<F16>(acc[2 * x] * inv, acc[2 * x + 1] * inv);
         if (p.lse && lane == 0)
             p.lse[(size_t)hq * p.T + tok] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
     }
@@ -1076,13 +1103,12 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     if (e != cudaSuccess) return e;
     k_paged_attn<F16, D, NQ, SEL><<<grid, kPaThreads, smem, stream>>>(P, qmap, kmap, vmap);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (SEL && P.splits == 1) return cudaSuccess;
+    // nothing is cut where whole units fill the rounds
+    if (SEL && (long long)P.a.T * P.a.hkv % grid == 0) return cudaSuccess;
     // The merge is launched while the attention kernel still runs and waits for its end
     // (programmatic dependent launch): its launch costs nothing then.
-    const int units = SEL ? P.a.T * P.a.hkv : grid;
-    const int rows = NQ * 128;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)units, (unsigned)std::min(NQ * 4, (P.a.G * (SEL ? 1 : NQ * P.tpt) + 7) / 8));
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(NQ * 4, (P.a.G * (SEL ? 1 : NQ * P.tpt) + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -1090,7 +1116,7 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_merge<F16, D, SEL>, P, rows, units);
+    return cudaLaunchKernelEx(&cfg, k_paged_merge<F16, D>, P, NQ * 128);
 }
 
 template <int F16, int D>
@@ -1129,12 +1155,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     P.tpt = sel ? 1 : kTileRows / a.G;
     P.box_rows = std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys);
     int grid = std::min(num_sms, kMaxStatusCtas);
-    P.splits = 1;
     if (sel) {
-        const long long units = (long long)a.T * a.hkv;
-        const int tiles = (a.topk * a.bs + kTileKeys - 1) / kTileKeys;
-        if (units * 2 <= grid) P.splits = std::max(1, std::min(tiles, (int)(grid / units)));
-        grid = (int)std::min<long long>(grid, units * P.splits);
+        P.cost_sel = (a.topk * a.bs + kTileKeys - 1) / kTileKeys + kUnitCost;
+        grid = (int)std::min<long long>(grid, (long long)a.T * a.hkv * P.cost_sel);
     }
     CUtensorMap qmap, kmap, vmap;
     const cuuint64_t qdims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.hq, (cuuint64_t)a.T};
