@@ -13,7 +13,9 @@
 //   all keys         the (unit, key tile) pairs of all units form one line that is cut into
 //                    one equal piece per CTA (one CTA per SM), whatever the lengths are; a
 //                    unit cut by a piece's end leaves fp32 partial results that
-//                    k_paged_merge joins in a fixed order.
+//                    k_paged_merge joins in a fixed order.  Where whole units, dealt out
+//                    evenly, take no longer than equal pieces and their merge
+//                    (kMergeCost), nothing is cut.
 //   selected blocks  a unit is one token and walks the list of its valid blocks.  Units go
 //                    round the CTAs, all tokens of a KV head before the next head, so that
 //                    the tokens of a chunk find the head's blocks in L2; the units that do
@@ -25,9 +27,9 @@
 //           (single tokens and short chunks: K and V are read once from memory, which
 //           bounds them).
 //
-//   warps 0-7    softmax, one warpgroup per stream, one thread per query row; epilogue
+//   warps 0-7    softmax and epilogue: a warpgroup per stream, one thread per query row
 //   warp 8       TMA producer: Q tiles, K and V tiles page by page through the block table
-//   warp 9       MMA issuer
+//   warps 9, 11  MMA issuers, one per stream
 //   warp 10      scheduler: walks the CTA's pieces of work ahead of the others and hands
 //                them over through a ring in shared memory
 //
@@ -46,11 +48,13 @@ namespace nsa {
 namespace {
 
 constexpr int kPaThreads = 384;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kPaThreads * 168, "registers of the launch");
 constexpr int kTileKeys = 128;
 constexpr int kRegion = kTileKeys * 128;     // bytes of 128 rows x 64 columns
 constexpr int kUnitCost = 1;                 // a unit's prologue and epilogue, in key tiles
+constexpr int kMergeCost = 6;                // writing and joining partial results, in key tiles
 constexpr float kLazy = 8.f;
 
 // A CTA's share of a unit: key tiles [p0, p1) of its nt.
@@ -79,7 +83,7 @@ struct alignas(1024) PaSmem {
     uint64_t ring_full[kRing], ring_empty[kRing];
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
     uint64_t xbar, drain;
     uint32_t tmem_base;
     int abort_flag, err;
@@ -133,9 +137,6 @@ __device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const float* v) {
         : "memory");
 }
 
-template <int I>
-struct Stream { static constexpr int value = I; };
-
 // Request r: rows [a, a + n) of q, kv keys, all inside their buffers whatever the arrays say.
 struct Req { int a, n, kv; };
 __device__ __forceinline__ Req request(const PagedAttnArgs& p, int r) {
@@ -181,7 +182,9 @@ struct WalkAll {
     long long x, x1, u0, total, pieces;
     long long unit_at;    // place of the piece's unit on the line
     int head, r, qt;
-    __device__ __forceinline__ static int tile_cost(const PagedAttnArgs& p, const Req& q, int i, int tpu) {
+    bool whole;           // a unit is one place: nothing is cut
+    __device__ __forceinline__ int tile_cost(const PagedAttnArgs& p, const Req& q, int i, int tpu) const {
+        if (whole) return 1;
         int pos0, lo, hi, nt;
         unit_keys(q, i * tpu, min(tpu, q.n - i * tpu), p.swin, &pos0, &lo, &hi, &nt);
         return nt + kUnitCost;
@@ -195,7 +198,7 @@ struct WalkAll {
         return v;
     }
     // every lane's own request
-    __device__ __forceinline__ static long long cost(const PagedAttnArgs& p, const Req& q, int tpu, int lane) {
+    __device__ __forceinline__ long long cost(const PagedAttnArgs& p, const Req& q, int tpu, int lane) const {
         const int tiles = (q.n + tpu - 1) / tpu;
         long long c = 0;
         if (tiles <= 2)
@@ -215,8 +218,10 @@ struct WalkAll {
     __device__ __forceinline__ bool start(const Params& P, int tpu, int cta, int grid, int lane) {
         const PagedAttnArgs& p = P.a;
         const int per = (p.R + 31) / 32;
-        long long mine = 0;
+        long long mine = 0, count = 0;
+        int most = 0;                       // costs of the most expensive unit
         bool good = true;
+        whole = false;
         auto load = [&](int i, int end) {
             Req q{0, 0, 0};
             if (i < end) q = request(p, i);
@@ -227,6 +232,17 @@ struct WalkAll {
             const Req q = load(i, p.R);
             if (i < p.R) good &= request_ok(p, i);
             mine += cost(p, q, tpu, lane);
+            const int last = (q.n + tpu - 1) / tpu - 1;
+            count += last + 1;
+            if (last >= 0)                  // (the last tile of tokens sees as many keys as any)
+                most = max(most, max(tile_cost(p, q, last, tpu), tile_cost(p, q, max(last - 1, 0), tpu)));
+        }
+        {
+            const long long units = __shfl_sync(0xffffffffu, scan(count, lane), 31) * p.hkv;
+            const long long line = __shfl_sync(0xffffffffu, scan(mine, lane), 31) * p.hkv;
+            most = __reduce_max_sync(0xffffffffu, most);
+            whole = (units + grid - 1) / grid * most <= (line + grid - 1) / grid + kMergeCost;
+            if (whole) mine = count;
         }
         const long long inc = scan(mine, lane);
         const long long all = __shfl_sync(0xffffffffu, inc, 31);
@@ -287,11 +303,11 @@ struct WalkAll {
             k.r = r;
             unit_keys(q, t, k.ntok, p.swin, &k.pos0, &k.lo, &k.hi, &k.nt);
             k.tile0 = k.lo / kTileKeys;
-            const long long cost = k.nt + kUnitCost, from = u0, u1 = min(cost, u0 + (x1 - x));
+            const long long cost = whole ? 1 : k.nt + kUnitCost, from = u0, u1 = min(cost, u0 + (x1 - x));
             unit_at = x - u0;
             x += u1 - u0;
             if (u1 == cost) { ++qt; u0 = 0; } else u0 = u1;
-            if (piece_tiles(from, u1, cta, k)) return true;
+            if (piece_tiles(from, whole ? k.nt : u1, cta, k)) return true;
         }
         return false;
     }
@@ -399,7 +415,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const PagedAttnArgs& p = P.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // roles: hardware warps 0-3 are 8-11 below, so that the issuer is not the last its
+    // scheduler picks
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = (tid >> 5) < 4 ? kSoftmaxWarps + (tid >> 5) : (tid >> 5) - 4;
     const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
     const int tpu = NQ * P.tpt;
 
@@ -408,23 +427,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         S.err = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.q_full[i], 1);
-            mbar_init(&S.q_empty[i], 1);
+            mbar_init(&S.q_empty[i], 2);
             mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_half[i], 4);
             mbar_init(&S.p_full[i], 4);
-            mbar_init(&S.pv_done[i], 1);
             mbar_init(&S.o_full[i], 1);
             mbar_init(&S.o_empty[i], NQ == 2 ? 4 : 8);
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&S.kv_full[i], 1);
-            mbar_init(&S.kv_empty[i], 1);
+            mbar_init(&S.kv_empty[i], NQ);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&S.ring_full[i], 1);
-            mbar_init(&S.ring_empty[i], 10);   // producer, issuer, eight softmax warps
+            mbar_init(&S.ring_empty[i], 3 + kSoftmaxWarps);   // producer, issuers, softmax
         }
-        mbar_init(&S.xbar, 8);
-        mbar_init(&S.drain, 1);
+        mbar_init(&S.xbar, kSoftmaxWarps);
+        mbar_init(&S.drain, 2);
         fence_barrier_init();
     }
     if (warp == 8) {
@@ -432,7 +451,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         tmem_alloc(&S.tmem_base, 512);
         tmem_relinquish();
     }
-    if (tid == 11 * 32) {
+    if (warp == 10 && lane == 0) {
         prefetch_tmap(&qmap);
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -470,14 +489,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     };
 
     // setmaxnreg at the head of each role: the compiler gives the code behind it that many
-    if (warp >= 8) {
+    if (warp >= kSoftmaxWarps) {
         set_regs_dec<kOtherRegs>();
     if (warp == 8) {
         // ------------------------------------------------------------- TMA producer
         const int boxes = kTileKeys / P.box_rows;      // per tile and 64-column half
         const int box = lane / kHalves, half = lane - box * kHalves;
         const uint32_t box_bytes = (uint32_t)P.box_rows * 128u;
-        int n = 0;                  // tiles put into the stages
+        // Place n of the stage ring: K tiles at 0 and 2 t - 1 (NQ = 1) or 2 t (NQ = 2), V
+        // tiles at 2 t + 2 or 2 t + 1: the order of use, K K V K V K V .. or K V K V ..
+        int n = 0;
         int units = 0;              // units whose Q was loaded
         int at = -1;                // piece being loaded
         int j = 0, j_end = 0;       // its next key tile
@@ -557,8 +578,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 if (!(ok = load(&kmap, page, row, g, mask))) break;
                 ++pending;
                 ++j;
-                // the order of use: K K V K V .. V V (NQ = 1) or K V K V .. (NQ = 2)
                 if (pending < kAhead) continue;
+            } else if (NQ == 1) {
+                ++n;                // no K tile is left for this place
             }
             if (pending == 0) break;
             if (!(ok = load(&vmap, page_q[0], row_q[0], g_q[0], mask_q[0]))) break;
@@ -583,100 +605,109 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int i = max(n - kStages, 0); i < n; ++i) land(&S.kv_full[i % kStages], (i / kStages) & 1);
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // -------------------------------------------------------------- MMA issuer
-        // Two cursors over the same pieces: the products S run two items ahead of the
-        // products P V (an item: a key tile for one stream; items alternate between the
-        // streams).  S(i + 2) follows P V(i) of its stream on the in-order tensor pipe, which
-        // is what lets P share the columns of S.
-        // The 16 MMAs of an item are 1024 cycles of tensor work, so their issue has to stay
-        // well below that: addresses that every lane holds go through u(), which lets the
-        // compiler keep them and all offsets in uniform registers, the stream is a constant of
-        // the unrolled loop, and a piece's fields are read once.
+    } else if (warp != 10) {
+        // ------------------------------------------------------------- MMA issuers
+        // Warp 9 issues for stream 0, warp 11 for stream 1.  A stream's next S follows its
+        // P V on the in-order tensor pipe, which is what lets P share the columns of S.  The
+        // 16 MMAs of an item (a key tile of a stream) are 1024 cycles of tensor work; next to
+        // the busy softmax warps the code around them takes about as long, hence a warp per
+        // stream, everything but P waited for first, addresses that every lane holds through
+        // u() (the compiler then keeps them and all offsets in uniform registers), and a
+        // piece's fields read once.
         const uint32_t elected = elect_one();
         constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
         constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
         constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+        constexpr int step = NQ == 2 ? 1 : 2;
         auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-        const uint32_t tm = u(tmem);
+        const int st = (int)u(warp == 9 ? 0u : 1u);
+        const uint32_t tS = u(tmem + st * 128u), tO = u(tmem + 256u + st * 128u);
         const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
         const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024));
         const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), kRegion, 1024));
-        int n = 0;                        // stages used
-        int at_s = -1, at_o = -1;         // pieces
-        int js = 0, js_end = 0, jo = 0, jo_end = 0;
-        bool two_s = true, two_o = true;  // NQ = 2: the unit has rows in its second tile
-        bool head_s = false;              // S: the next item is the unit's first
+        uint64_t *const s_full = &S.s_full[st], *const p_half = &S.p_half[st], *const p_full = &S.p_full[st];
+        uint64_t *const o_full = &S.o_full[st],
+                 *const o_empty = &S.o_empty[st];
+        // two cursors over the pieces: the next S and the next P V; tile numbers over all
+        // pieces give the stages
+        int at_s = -1, js = 0, js_end = 0, base_s = 0, units_s = 0;
+        int at_o = -1, jo = 0, jo_end = 0, base_o = 0;
+        int count_s = 0, count_o = 0;     // key tiles of the pieces so far, both streams
+        bool rows_s = true, rows_o = true;   // the unit has rows in this stream's tile
+        int qb = 0;
+        bool head_s = false, first_o = true;
         int lo_o = 0, hi_o = 0, tile0_o = 0;
-        int units_s = 0;
-        int ks_stage = 0, vo_stage = 0;
+        int sums = 0, items = 0;          // sums completed, P V items
         bool ok = true, more_s = true, more_o = true;
-        int o_cnt[2] = {0, 0};            // sums each stream has completed
-        bool o_first[2] = {true, true};   // the stream's next P V starts a sum
-        int pv_cnt = 0;                   // P V items of a stream, before this pair
-        auto advance_s = [&]() {          // to the piece of the next S
-            while (ok && more_s && js == js_end) {
-                if (!(ok = fetch(++at_s))) return;
+        auto first_tile = [&](int p0, int count) { return NQ == 2 ? p0 : p0 + ((count & 1) ^ st); };
+        // to the next S; everything it waits for.  more_s: there is one
+        auto prepare_s = [&]() -> bool {
+            while (more_s && js >= js_end) {
+                if (!fetch(++at_s)) return false;
                 const Piece& k = S.ring[at_s % kRing];
                 more_s = k.more != 0;
-                js = k.p0;
-                js_end = k.p1;
-                two_s = NQ == 2 && k.ntok > P.tpt;
-                if (more_s && js < js_end) { ++units_s; head_s = true; }
+                const int p0 = k.p0, nt = k.p1 - p0;
+                if (!more_s || nt == 0) continue;
+                qb = NQ == 2 ? 0 : units_s & 1;
+                ++units_s;
+                js = first_tile(p0, count_s);
+                js_end = p0 + nt;
+                base_s = count_s - p0;
+                count_s += nt;
+                rows_s = NQ == 1 || st == 0 || k.ntok > P.tpt;
+                head_s = true;
+                if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);   // no tile for this stream
             }
-        };
-        auto advance_o = [&]() {
-            while (ok && more_o && jo == jo_end) {
-                if (at_o >= 0) release(at_o);
-                if (!(ok = fetch(++at_o))) return;
-                const Piece& k = S.ring[at_o % kRing];
-                more_o = k.more != 0;
-                jo = k.p0;
-                jo_end = k.p1;
-                two_o = NQ == 2 && k.ntok > P.tpt;
-                lo_o = k.lo;
-                hi_o = k.hi;
-                tile0_o = k.tile0;
-                o_first[0] = o_first[1] = true;
-            }
-        };
-        auto issue_s = [&](auto stream) -> bool {
-            constexpr int st = decltype(stream)::value;
-            constexpr int qsub = NQ == 2 ? st : 0;
-            const int qb = NQ == 2 ? 0 : (units_s - 1) & 1;
-            if (head_s && qsub == 0) {
+            if (!more_s) return true;
+            if (head_s) {
                 const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
                 if (!wait(&S.q_full[qb], use & 1)) return false;
                 head_s = false;
             }
-            if (qsub == 0) {
-                ks_stage = n % kStages;
-                if (!wait(&S.kv_full[ks_stage], (n / kStages) & 1)) return false;
-                ++n;
-            }
-            tc_fence_after();
-            if (qsub == 0 || two_s) {
-                const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? qsub : qb) * kTileU);
-                const uint32_t b0 = u(k_desc0 + (uint32_t)ks_stage * kTileU);
+            const int t = base_s + js, n = NQ == 2 ? 2 * t : max(2 * t - 1, 0);
+            return wait(&S.kv_full[n % kStages], (n / kStages) & 1);
+        };
+        auto issue_s = [&]() {
+            const int t = base_s + js, stg = (NQ == 2 ? 2 * t : max(2 * t - 1, 0)) % kStages;
+            const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? st : qb) * kTileU);
+            const uint32_t b0 = u(k_desc0 + (uint32_t)stg * kTileU);
+            if (rows_s) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t off = (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2);
-                    mma_ss_e(tm + st * 128u, a0 + off, b0 + off, kIdescS, x > 0 ? 1u : 0u, elected);
+                    mma_ss_e(tS, a0 + off, b0 + off, kIdescS, x > 0 ? 1u : 0u, elected);
                 }
             }
-            mma_commit_e(&S.s_full[st], elected);
-            if (NQ == 1 || qsub == 1) {
-                mma_commit_e(&S.kv_empty[ks_stage], elected);
-                ++js;
-                if (js == js_end) mma_commit_e(&S.q_empty[qb], elected);
-            }
-            return true;
+            mma_commit_e(s_full, elected);
+            mma_commit_e(&S.kv_empty[stg], elected);
+            js += step;
+            if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
         };
-        auto issue_pv = [&](auto stream) -> bool {
-            constexpr int st = decltype(stream)::value;
-            constexpr int qsub = NQ == 2 ? st : 0;
+        ok = prepare_s();
+        if (ok && more_s) issue_s();
+        while (ok) {
+            while (more_o && jo >= jo_end) {
+                if (at_o >= 0) release(at_o);
+                if (!(ok = fetch(++at_o))) break;
+                const Piece& k = S.ring[at_o % kRing];
+                more_o = k.more != 0;
+                const int p0 = k.p0, nt = k.p1 - p0;
+                if (!more_o || nt == 0) continue;
+                jo = first_tile(p0, count_o);
+                jo_end = p0 + nt;
+                base_o = count_o - p0;
+                count_o += nt;
+                rows_o = NQ == 1 || st == 0 || k.ntok > P.tpt;
+                lo_o = k.lo;
+                hi_o = k.hi;
+                tile0_o = k.tile0;
+                first_o = true;
+            }
+            if (!ok || !more_o) break;
+            const int t = base_o + jo, n = NQ == 2 ? 2 * t + 1 : 2 * t + 2, stg = n % kStages;
+            if (!(ok = wait(&S.kv_full[stg], (n / kStages) & 1))) break;
             // the tile's visible columns; all of them but at a piece's ends
-            int l0 = 0, h0 = 63, l1 = 64, h1 = 127;
+            int l0, h0, l1, h1;
             if (SEL) {
                 tile_cols<SEL>(P, S.ring[at_o % kRing], S.list[at_o % kRing], jo, l0, h0, l1, h1);
             } else {
@@ -687,83 +718,64 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 l1 = max(l0, 64);
             }
             const bool full = l0 == 0 && h0 == 63 && l1 == 64 && h1 == 127;
-            if (qsub == 0) {
-                vo_stage = n % kStages;
-                if (!wait(&S.kv_full[vo_stage], (n / kStages) & 1)) return false;
-                ++n;
-                if (!full) {   // clear the rows of the used 16-key steps that nobody may see
-                    uint8_t* v = S.kv[vo_stage][0];
-                    auto clear = [&](int from, int to) {
-                        for (int r = from; r < to; ++r)
-                            if (lane < 8 * kHalves)
-                                *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    };
-                    if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
-                    if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
-                    fence_async_smem();
-                    __syncwarp();
-                }
+            if (!full) {
+                // clear the rows of the used 16-key steps that nobody may see (NQ = 2: both
+                // issuers do, each before its own products)
+                uint8_t* v = S.kv[stg][0];
+                auto clear = [&](int from, int to) {
+                    for (int r = from; r < to; ++r)
+                        if (lane < 8 * kHalves)
+                            *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                };
+                if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
+                if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
+                fence_async_smem();
+                __syncwarp();
             }
-            if (o_first[st] && o_cnt[st] > 0 && !wait(&S.o_empty[st], (o_cnt[st] - 1) & 1)) return false;
-            if (!wait(&S.p_full[st], pv_cnt & 1)) return false;
+            if (first_o && sums > 0 && !(ok = wait(o_empty, (sums - 1) & 1))) break;
+            if (!(ok = prepare_s())) break;
+            const uint32_t b0 = u(v_desc0 + (uint32_t)stg * kTileU);
+            uint32_t acc = first_o ? 0u : 1u;
+            if (!(ok = wait(p_half, items & 1))) break;
             tc_fence_after();
-            if (qsub == 0 || two_o) {
-                const uint32_t b0 = u(v_desc0 + (uint32_t)vo_stage * kTileU);
-                const uint32_t tP = tm + st * 128u, tO = tm + 256u + st * 128u;
-                uint32_t acc = o_first[st] ? 0u : 1u;
-                if (full) {
+            if (rows_o && full) {         // the first 64 keys while the rows work on the others
 #pragma unroll
-                    for (int x = 0; x < kTileKeys / 16; ++x)
-                        mma_ts_e(tO, tP + x * 8u, b0 + x * 128u, kIdescO, x == 0 ? acc : 1u, elected);
-                } else {
+                for (int x = 0; x < 4; ++x)
+                    mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, x == 0 ? acc : 1u, elected);
+            }
+            if (!(ok = wait(p_full, items & 1))) break;
+            tc_fence_after();
+            if (rows_o && full) {
+#pragma unroll
+                for (int x = 4; x < 8; ++x) mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, 1u, elected);
+            } else if (rows_o) {
 #pragma unroll 1
-                    for (int x = 0; x < kTileKeys / 16; ++x) {
-                        const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
-                                               : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
-                        if (use) {
-                            mma_ts_e(tO, tP + x * 8u, b0 + x * 128u, kIdescO, acc, elected);
-                            acc = 1u;
-                        }
+                for (int x = 0; x < kTileKeys / 16; ++x) {
+                    const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
+                                           : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
+                    if (use) {
+                        mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, acc, elected);
+                        acc = 1u;
                     }
                 }
             }
-            o_first[st] = false;
-            mma_commit_e(&S.pv_done[st], elected);
-            // the stream's last item of the unit: O is complete
-            if (NQ == 2 ? jo + 1 == jo_end : jo + 2 >= jo_end) {
-                mma_commit_e(&S.o_full[st], elected);
-                ++o_cnt[st];
+            first_o = false;
+            mma_commit_e(&S.kv_empty[stg], elected);
+            jo += step;
+            ++items;
+            if (jo >= jo_end) {               // the stream's last item of the unit: O is complete
+                mma_commit_e(o_full, elected);
+                ++sums;
             }
-            if (NQ == 1 || qsub == 1) {
-                mma_commit_e(&S.kv_empty[vo_stage], elected);
-                ++jo;
-            }
-            return true;
-        };
-        advance_s();
-        if (ok && more_s) ok = issue_s(Stream<0>{});
-        advance_s();
-        if (ok && more_s) ok = issue_s(Stream<1>{});
-        while (ok) {
-            advance_o();
-            if (!ok || !more_o) break;
-            if (!(ok = issue_pv(Stream<0>{}))) break;
-            advance_s();
-            if (ok && more_s) ok = issue_s(Stream<0>{});
-            advance_o();
-            if (!ok || !more_o) break;
-            if (!(ok = issue_pv(Stream<1>{}))) break;
-            advance_s();
-            if (ok && more_s) ok = issue_s(Stream<1>{});
-            ++pv_cnt;
+            if (more_s) issue_s();
         }
         mma_commit_e(&S.drain, elected);
         {
             const long long start = clock64();
             while (!mbar_try_wait(&S.drain, 0) && clock64() - start < kWaitBudgetCycles) {}
         }
-    } else if (warp == 10) {
+    } else {
         // --------------------------------------------------------------- scheduler
         WalkAll wall{};
         WalkSel wsel{};
@@ -803,7 +815,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // ------------------------------------------------------- softmax and epilogue
         const int st = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + lane_off + (uint32_t)st * 128u;
+        const uint32_t tS = tmem + lane_off + (uint32_t)st * 128u, tO = tmem + lane_off + 256u;
         const int rt = row / p.G, head = row - rt * p.G;
         const float c = p.scale_log2;
         int items = 0;                    // this stream's items so far
@@ -819,28 +831,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const int ti = NQ == 2 ? st * P.tpt + rt : rt;         // token within the unit
             const bool valid = rt < P.tpt && ti < k.ntok;
             const int pos = k.pos0 + ti;
-            const int row_lo = SEL ? k.lo : (p.swin > 0 ? max(0, pos - p.swin + 1) : 0);
+            const int row_lo = !SEL && p.swin > 0 ? max(0, pos - p.swin + 1) : 0;
             const bool active = __any_sync(0xffffffffu, valid);
+            const int p0 = k.p0, p1 = k.p1, nt = p1 - p0;
             float m = -CUDART_INF_F, l = 0.f;
-            bool first = true;
             // NQ = 1: key tiles of the piece alternate between the streams, from where the
             // last unit left off
             const int step = NQ == 2 ? 1 : 2;
-            const int from = NQ == 2 ? k.p0 : k.p0 + ((tiles & 1) ^ st);
-            for (int j = from; j < k.p1; j += step, ++items) {
+            const int from = NQ == 2 ? p0 : p0 + ((tiles & 1) ^ st);
+            for (int j = from; j < p1; j += step, ++items) {
                 if (!(ok = wait(&S.s_full[st], items & 1))) break;
                 if (active) {
                     tc_fence_after();
                     float s[128];
                     tmem_ld64_sync(tS, s);
                     tmem_ld64_sync(tS + 64, s + 64);
-                    int l0, h0, l1, h1;
-                    tile_cols<SEL>(P, k, list, j, l0, h0, l1, h1);
-                    if (!SEL) {
+                    int l0, h0, l1, h1;   // this row's visible columns
+                    if (SEL) {
+                        tile_cols<SEL>(P, k, list, j, l0, h0, l1, h1);
+                    } else {
                         const int key0 = (k.tile0 + j) * kTileKeys;
-                        l0 = valid ? row_lo - key0 : 0;
+                        l0 = l1 = valid ? row_lo - key0 : 0;
                         h0 = h1 = valid ? pos - key0 : 127;
-                        l1 = l0;
                     }
                     if (__any_sync(0xffffffffu, l0 > 0 || h0 < 63 || l1 > 64 || h1 < 127)) {
 #pragma unroll
@@ -860,96 +872,90 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         const float a = grow ? ex2_approx(m - top) : 1.f;   // m = -inf: 0
                         if (grow) m = top;
                         l *= a;
-                        if (!first) {
-                            if (!(ok = wait(&S.pv_done[st], (items - 1) & 1))) break;
-                            tc_fence_after();
-                            const uint32_t tO = tmem + lane_off + 256u + (uint32_t)st * 128u;
+                        if (j != from) {
+                            // (the products before this S, P V of the last tile among them,
+                            // are complete)
 #pragma unroll 1
                             for (int x = 0; x < D; x += 16) {
                                 float o[16];
-                                tmem_ld16_sync(tO + x, o);
+                                tmem_ld16_sync(tO + (uint32_t)(st * 128 + x), o);
 #pragma unroll
                                 for (int y = 0; y < 16; ++y) o[y] *= a;
-                                tmem_st16_sync(tO + x, o);
+                                tmem_st16_sync(tO + (uint32_t)(st * 128 + x), o);
                             }
                         }
                     }
-                    first = false;
                     const float mm = m == -CUDART_INF_F ? 0.f : m;
                     const float2 c2 = make_float2(c, c), m2 = make_float2(-mm, -mm);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    uint32_t pk[64];
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        float2 e = fma2(make_float2(s[2 * x], s[2 * x + 1]), c2, m2);
-                        e.x = ex2_approx(e.x);
-                        e.y = ex2_approx(e.y);
-                        sum[x & 1] = add2(sum[x & 1], e);
-                        pk[x] = pack2<F16>(e.x, e.y);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            float2 e = fma2(make_float2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, m2);
+                            e.x = ex2_approx(e.x);
+                            e.y = ex2_approx(e.y);
+                            sum[x & 1] = add2(sum[x & 1], e);
+                            pk[x] = pack2<F16>(e.x, e.y);
+                        }
+                        tmem_st32_sync(tS + 32 * h, pk);
+                        tc_fence_before();
+                        if (h == 0) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&S.p_half[st]);
+                        }
                     }
-                    tmem_st32_sync(tS, pk);
-                    tmem_st32_sync(tS + 32, pk + 32);
                     const float2 t2 = add2(sum[0], sum[1]);
                     l += t2.x + t2.y;
-                    tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_full[st]);
+                if (lane == 0) {
+                    if (!active) mbar_arrive(&S.p_half[st]);
+                    mbar_arrive(&S.p_full[st]);
+                }
             }
             if (!ok) break;
-            const int nt = k.p1 - k.p0;
             const int n0 = NQ == 2 ? nt : (nt + 1 - (tiles & 1)) >> 1, n1 = NQ == 2 ? nt : nt - n0;
             tiles += nt;
-            const uint32_t tO = tmem + lane_off + 256u;
-            if (NQ == 2) {
-                if (nt > 0) {
-                    if (!(ok = wait(&S.o_full[st], o_cnt[st] & 1))) break;
-                    ++o_cnt[st];
-                    tc_fence_after();
+            float w0 = 0.f, w1 = 0.f;         // weights of the streams' sums
+            if (nt > 0) {
+                if (NQ == 2) {
+                    if (!(ok = wait(&S.o_full[st], o_cnt[st]++ & 1))) break;
+                } else {
+                    S.xch[units & 1][st][row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.xbar);
+                    ok = wait(&S.xbar, units & 1);
+                    if (ok && n0 > 0) ok = wait(&S.o_full[0], o_cnt[0]++ & 1);
+                    if (ok && n1 > 0) ok = wait(&S.o_full[1], o_cnt[1]++ & 1);
+                    if (!ok) break;
+                    const float2 a = S.xch[units & 1][0][row], b = S.xch[units & 1][1][row];
+                    m = fmaxf(a.x, b.x);
+                    w0 = a.y != 0.f ? ex2_approx(a.x - m) : 0.f;   // (a NaN sum stays one)
+                    w1 = b.y != 0.f ? ex2_approx(b.x - m) : 0.f;
+                    l = w0 * a.y + w1 * b.y;
                 }
-            } else if (nt > 0) {
-                // both streams' (m, l) of every row
-                S.xch[units & 1][st][row] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.xbar);
-                ok = wait(&S.xbar, units & 1);
-                if (ok && n0 > 0) {
-                    ok = wait(&S.o_full[0], o_cnt[0] & 1);
-                    ++o_cnt[0];
-                }
-                if (ok && n1 > 0) {
-                    ok = wait(&S.o_full[1], o_cnt[1] & 1);
-                    ++o_cnt[1];
-                }
-                if (!ok) break;
                 tc_fence_after();
             }
-            // weights of the streams' sums
-            float w0 = 0.f, w1 = 0.f;
-            if (NQ == 1 && nt > 0) {
-                const float2 a = S.xch[units & 1][0][row], b = S.xch[units & 1][1][row];
-                m = fmaxf(a.x, b.x);
-                w0 = a.y > 0.f ? ex2_approx(a.x - m) : 0.f;
-                w1 = b.y > 0.f ? ex2_approx(b.x - m) : 0.f;
-                if (!(a.y == a.y) || !(b.y == b.y)) w0 = w1 = CUDART_NAN_F;
-                l = w0 * a.y + w1 * b.y;
-            }
             const int tok = k.tok0 + ti, hq = k.g * p.G + head;
+            const int slot = k.slot;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
-            // NQ = 1: each warpgroup takes half of the columns; NQ = 2: each its own rows
+            // NQ = 1: each warpgroup takes half of the columns of every row
             constexpr int kCols = NQ == 2 ? D : D / 2;
             const int col0 = NQ == 2 ? 0 : st * kCols;
+            const size_t part = (size_t)slot * (NQ * 128) + (NQ == 2 ? st * 128 : 0) + row;
             if (active) {
 #pragma unroll 1
-                for (int x = 0; x < kCols; x += 16) {
+                for (int x = col0; x < col0 + kCols; x += 16) {
                     float o[16];
                     if (NQ == 2) {
-                        if (nt > 0) tmem_ld16_sync(tO + (uint32_t)(st * 128 + x), o);
+                        tmem_ld16_sync(tO + (uint32_t)(st * 128 + x), o);
                     } else {
                         // a weight of 0 belongs to a sum that may never have been started
                         float o1[16];
-                        tmem_ld16_sync(tO + (uint32_t)(col0 + x), o);
-                        tmem_ld16_sync(tO + (uint32_t)(128 + col0 + x), o1);
+                        tmem_ld16_sync(tO + (uint32_t)x, o);
+                        tmem_ld16_sync(tO + (uint32_t)(128 + x), o1);
 #pragma unroll
                         for (int y = 0; y < 16; ++y)
                             o[y] = (w0 != 0.f ? w0 * o[y] : 0.f) + (w1 != 0.f ? w1 * o1[y] : 0.f);
@@ -959,8 +965,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                         for (int y = 0; y < 16; ++y) o[y] = 0.f;
                     }
                     if (!valid) continue;
-                    if (k.slot < 0) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)tok * p.hq + hq) * D + col0 + x);
+                    if (slot < 0) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)tok * p.hq + hq) * D + x);
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
                             dst[y] = make_uint4(pack2<F16>(o[8 * y] * inv, o[8 * y + 1] * inv),
@@ -968,21 +974,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                                                 pack2<F16>(o[8 * y + 4] * inv, o[8 * y + 5] * inv),
                                                 pack2<F16>(o[8 * y + 6] * inv, o[8 * y + 7] * inv));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(
-                            P.part_o + ((size_t)k.slot * (NQ * 128) + (NQ == 2 ? st * 128 : 0) + row) * D + col0 + x);
+                        float4* dst = reinterpret_cast<float4*>(P.part_o + part * D + x);
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                     }
                 }
-                if (valid && (NQ == 2 || st == 0)) {
-                    if (k.slot < 0) {
-                        if (p.lse)
-                            p.lse[(size_t)hq * p.T + tok] =
-                                l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
-                    } else {
-                        P.part_ml[(size_t)k.slot * (NQ * 128) + (NQ == 2 ? st * 128 : 0) + row] = make_float2(m, l);
-                    }
+                if (valid && col0 == 0) {
+                    if (slot >= 0)
+                        P.part_ml[part] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[(size_t)hq * p.T + tok] =
+                            l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
             if (nt > 0) {
