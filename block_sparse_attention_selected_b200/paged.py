@@ -22,10 +22,17 @@ import ctypes
 
 import torch
 
-from . import NSA_F16, NsaError, _check, _need, get_workspace, load_library
+from . import NSA_F16, NsaError, _check, _need, _ws_cache, get_workspace, load_library
 
 __all__ = ["nsa_sel_paged_plan", "nsa_sel_paged_write_kv", "nsa_sel_paged_attn_workspace_size",
            "nsa_sel_paged_attn_fwd", "nsa_sel_paged_sel_fwd"]
+
+# A decode step makes these calls once per layer on kernels of a few microseconds, so the
+# host path is kept short: plain comparisons, and the stream and device queries that
+# torch's own generated code uses.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_ELEM = {torch.bfloat16: 0, torch.float16: NSA_F16}
 
 
 class _Cache(ctypes.Structure):   # nsa_paged_cache_t
@@ -38,22 +45,20 @@ class _Cache(ctypes.Structure):   # nsa_paged_cache_t
 def _call(fn: str, dev: torch.device, *args):
     """Calls the library with the tensors' device current."""
     f = getattr(load_library(), fn)
-    if dev.index == torch.cuda.current_device():
-        _check(fn, f(*args))
+    if dev.index == _current_device():
+        code = f(*args)
     else:
         with torch.cuda.device(dev):
-            _check(fn, f(*args))
-
-
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+            code = f(*args)
+    if code:
+        _check(fn, code)
 
 
 def _need_strided(t, name, dtype, ndim, dev):
     """A CUDA tensor whose last dimension is adjacent; other strides are free."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -61,39 +66,40 @@ def _need_strided(t, name, dtype, ndim, dev):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{name} must have adjacent columns (stride 1 in its last dimension)")
 
 
 def _strides(t):
     # an empty tensor may have any strides; nothing is read through them
-    return (t.stride(0), t.stride(1)) if t.numel() else (0, 0)
+    return t.stride()[:2] if t.numel() else (0, 0)
 
 
 def _cache_arg(k_cache, v_cache, et, dev):
     _need_strided(k_cache, "k_cache", et, 4, dev)
     _need_strided(v_cache, "v_cache", et, 4, dev)
-    if k_cache.shape != v_cache.shape:
+    shape, strides = k_cache.shape, k_cache.stride()
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if k_cache.stride() != v_cache.stride():
+    if strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same strides")
-    pages, page, hkv, d = k_cache.shape
-    sp, st, sh, _ = k_cache.stride()
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, pages, page, hkv, d)
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides[:3], *shape)
 
 
 def _elem(t, name):
-    if t.dtype == torch.bfloat16:
-        return torch.bfloat16, 0
-    if t.dtype == torch.float16:
-        return torch.float16, NSA_F16
-    raise TypeError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
+    et = t.dtype
+    if et not in _ELEM:
+        raise TypeError(f"{name}: expected bfloat16 or float16, got {et}")
+    return et, _ELEM[et]
 
 
-def _need_table(block_table, R, dev):
+def _table_arg(block_table, R, dev):
+    """(pointer, width, row stride) of a block table of R rows."""
     _need_strided(block_table, "block_table", torch.int32, 2, dev)
-    if block_table.shape[0] != R:
+    rows, width = block_table.shape
+    if rows != R:
         raise ValueError("block_table needs one row per request")
+    return block_table.data_ptr(), width, max(block_table.stride(0), width) if R == 1 else block_table.stride(0)
 
 
 def nsa_sel_paged_plan(new_lens, cached_lens, free_pages, block_table, page_size, total_tokens):
@@ -114,19 +120,15 @@ def nsa_sel_paged_plan(new_lens, cached_lens, free_pages, block_table, page_size
     R, T = new_lens.shape[0], int(total_tokens)
     if cached_lens.shape[0] != R:
         raise ValueError("new_lens and cached_lens must have the same length")
-    _need_table(block_table, R, dev)
+    table = _table_arg(block_table, R, dev)
     if T < 0:
         raise ValueError("total_tokens must not be negative")
-    cu = torch.empty(R + 1, dtype=torch.int32, device=dev)
-    kv_lens = torch.empty(R, dtype=torch.int32, device=dev)
-    slots = torch.empty(T, dtype=torch.int64, device=dev)
-    positions = torch.empty(T, dtype=torch.int32, device=dev)
-    used = torch.empty(1, dtype=torch.int32, device=dev)
+    cu, kv_lens, used = new_lens.new_empty(R + 1), new_lens.new_empty(R), new_lens.new_empty(1)
+    slots, positions = new_lens.new_empty(T, dtype=torch.int64), new_lens.new_empty(T)
     _call("nsa_sel_paged_plan", dev, new_lens.data_ptr(), cached_lens.data_ptr(), R,
-          free_pages.data_ptr(), free_pages.shape[0], block_table.data_ptr(), block_table.shape[1],
-          max(block_table.stride(0), block_table.shape[1]) if R == 1 else block_table.stride(0),
-          int(page_size), T, cu.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(),
-          positions.data_ptr(), used.data_ptr(), _raw_stream(dev))
+          free_pages.data_ptr(), free_pages.shape[0], *table, int(page_size), T, cu.data_ptr(),
+          kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), used.data_ptr(),
+          _raw_stream(dev.index))
     return cu, kv_lens, slots, positions, used
 
 
@@ -141,11 +143,11 @@ def nsa_sel_paged_write_kv(k, v, slots, k_cache, v_cache):
     _need_strided(v, "v", et, 3, dev)
     _need(slots, "slots", torch.int64, 1, dev)
     cache = _cache_arg(k_cache, v_cache, et, dev)
-    if v.shape != k.shape or k.shape[0] != slots.shape[0] or k.shape[1:] != k_cache.shape[2:]:
+    shape = k.shape
+    if v.shape != shape or shape[0] != slots.shape[0] or shape[1] != cache.hkv or shape[2] != cache.head_dim:
         raise ValueError("inconsistent shapes")
-    _call("nsa_sel_paged_write_kv", dev, k.data_ptr(), v.data_ptr(), *_strides(k),
-          *_strides(v), slots.data_ptr(), k.shape[0], ctypes.byref(cache),
-          _raw_stream(dev))
+    _call("nsa_sel_paged_write_kv", dev, k.data_ptr(), v.data_ptr(), *_strides(k), *_strides(v),
+          slots.data_ptr(), shape[0], ctypes.byref(cache), _raw_stream(dev.index))
 
 
 def nsa_sel_paged_attn_workspace_size(total_tokens, num_seqs, hq, hkv, head_dim) -> int:
@@ -155,13 +157,20 @@ def nsa_sel_paged_attn_workspace_size(total_tokens, num_seqs, hq, hkv, head_dim)
     return int(n)
 
 
-def _paged_workspace(nbytes, dev):
+_workspace_bytes: dict = {}   # head_dim -> bytes: the size depends on nothing else
+
+
+def _paged_workspace(T, R, hq, hkv, d, dev, stream):
+    nbytes = _workspace_bytes.get(d)
+    if nbytes is None:
+        nbytes = _workspace_bytes[d] = nsa_sel_paged_attn_workspace_size(T, R, hq, hkv, d)
     # A call that is being captured takes its workspace from the graph's own memory: the
     # cached one would be shared with other graphs and with eager calls, which may overlap
     # with a replay.
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return get_workspace(nbytes, dev)
+    ws = _ws_cache.get((dev, stream))
+    return ws if ws is not None and ws.numel() >= nbytes else get_workspace(nbytes, dev)
 
 
 def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection, scale, window_size,
@@ -172,31 +181,31 @@ def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection
     cache = _cache_arg(k_cache, v_cache, et, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
     _need(kv_lens, "kv_lens", torch.int32, 1, dev)
-    T, hq, d = q.shape
+    T, hq, d = shape = q.shape
     R = kv_lens.shape[0]
-    _need_table(block_table, R, dev)
+    table = _table_arg(block_table, R, dev)
     if d != cache.head_dim or cu_seqlens.shape[0] != R + 1:
         raise ValueError("inconsistent shapes")
     if out is None:
-        out = torch.empty((T, hq, d), dtype=et, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(out, "out", et, 3, dev)
-        if out.shape != q.shape:
+        if out.shape != shape:
             raise ValueError("out must have the shape of q")
     if lse is not None:
         _need(lse, "lse", torch.float32, 2, dev)
         if lse.shape != (hq, T):
             raise ValueError("lse must be [hq, T]")
     elif with_lse:
-        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
-    nbytes = nsa_sel_paged_attn_workspace_size(T, R, hq, cache.hkv, d)
-    ws = workspace if workspace is not None else _paged_workspace(nbytes, dev)
-    _call(fn, dev, q.data_ptr(), *_strides(q), T, hq, ctypes.byref(cache),
-          cu_seqlens.data_ptr(), kv_lens.data_ptr(), R, block_table.data_ptr(), block_table.shape[1],
-          max(block_table.stride(0), block_table.shape[1]) if R == 1 else block_table.stride(0),
-          *selection, float(d ** -0.5 if scale is None else scale), int(window_size), out.data_ptr(),
-          lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(), _raw_stream(dev),
-          flag)
+        lse = q.new_empty((hq, T), dtype=torch.float32)
+    stream = _raw_stream(dev.index)
+    ws = workspace
+    if ws is None:
+        ws = _paged_workspace(T, R, hq, cache.hkv, d, dev, stream)
+    _call(fn, dev, q.data_ptr(), *_strides(q), T, hq, ctypes.byref(cache), cu_seqlens.data_ptr(),
+          kv_lens.data_ptr(), R, *table, *selection, float(d ** -0.5 if scale is None else scale),
+          int(window_size), out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
+          ws.numel(), stream, flag)
     return out, lse
 
 

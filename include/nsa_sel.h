@@ -409,7 +409,8 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  *                and those wholly before the window may hold anything.
  *   out          the type of q, [total_tokens, hq, head_dim] contiguous (written)
  *   lse          fp32 [hq, total_tokens] (written; natural log), or null
- *   workspace    of nsa_sel_paged_attn_workspace_size() bytes, 256-byte aligned; calls
+ *   workspace    of nsa_sel_paged_attn_workspace_size() bytes (0: unsupported sizes; else
+ *                it depends on head_dim alone), 256-byte aligned, contents arbitrary; calls
  *                that may overlap on the GPU need a workspace each
  * Cache rows that hold no visible key may hold anything, infinities and NaN too.  The
  * scale must be positive and finite.  Other flag bits return NSA_ERR_INVALID_ARG.
