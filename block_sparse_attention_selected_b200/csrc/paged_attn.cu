@@ -8,18 +8,7 @@
 // below 2^8 and fp32 sums lose nothing.  P is rounded to the 16-bit type of V for the
 // second product; l sums the unrounded weights.
 //
-// Work.  A unit is the rows of one KV head's query heads for up to NQ * floor(128 / G)
-// consecutive new tokens of one request (G query heads per KV head, rows token-major).
-//   all keys         the (unit, key tile) pairs of all units form one line that is cut into
-//                    one equal piece per CTA (one CTA per SM), whatever the lengths are; a
-//                    unit cut by a piece's end leaves fp32 partial results that
-//                    k_paged_merge joins in a fixed order.  Where whole units, dealt out
-//                    evenly, take no longer than equal pieces and their merge
-//                    (kMergeCost), nothing is cut.
-//   selected blocks  a unit is one token and walks the list of its valid blocks.  Units go
-//                    round the CTAs, all tokens of a KV head before the next head, so that
-//                    the tokens of a chunk find the head's blocks in L2; the units that do
-//                    not fill a last round form a line as above.
+// (paged_attn.cuh: units, their division among the CTAs, the scheduler and the producer.)
 // Two streams of (S, P, O) alternate on the tensor pipe, so that one stream's softmax runs
 // under the other's products:
 //   NQ = 2  two tiles of 128 query rows over the same key tiles (long chunks);
@@ -32,17 +21,10 @@
 //   warps 9, 11  MMA issuers, one per stream
 //   warp 10      scheduler: walks the CTA's pieces of work ahead of the others and hands
 //                them over through a ring in shared memory
-//
-// Keys that no row of a unit may see are never read into a product: their pages are not
-// loaded, and the issuer leaves out the 16-key steps of P V without a visible key and
-// clears the dead rows of V in the others (0 times infinity is not 0).
-#include <math_constants.h>
-
 #include <algorithm>
 #include <type_traits>
 
-#include "nsa_common.cuh"
-#include "nsa_kernels.h"
+#include "paged_attn.cuh"
 
 namespace nsa {
 namespace {
@@ -51,26 +33,6 @@ constexpr int kPaThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kPaThreads * 168, "registers of the launch");
-constexpr int kTileKeys = 128;
-constexpr int kRegion = kTileKeys * 128;     // bytes of 128 rows x 64 columns
-constexpr int kUnitCost = 1;                 // a unit's prologue and epilogue, in key tiles
-constexpr int kMergeCost = 6;                // writing and joining partial results, in key tiles
-constexpr float kLazy = 8.f;
-
-// A CTA's share of a unit: key tiles [p0, p1) of its nt.
-struct Piece {
-    int tok0, ntok, g, r;
-    int pos0;           // position of the first token
-    int lo, hi;         // keys that some row sees lie in [lo, hi]
-    int tile0;          // all keys: the first key tile's number
-    int nb;             // selected blocks: entries of the list
-    int p0, p1, nt;
-    int slot;           // partial slot, or -1: the piece is the whole unit
-    int more;           // 0: no piece, the CTA is done
-};
-
-constexpr int kRing = 8;
-
 template <int D>
 struct alignas(1024) PaSmem {
     static constexpr int kHalves = D / 64;
@@ -89,24 +51,6 @@ struct alignas(1024) PaSmem {
     int abort_flag, err;
 };
 
-struct Params {
-    PagedAttnArgs a;
-    int tpt;            // tokens per 128-row tile
-    int box_rows;       // rows of one K / V box
-    int cost_sel;       // selected blocks: places of a unit on the line
-    float* part_o;      // [pieces][NQ * 128][D]
-    float2* part_ml;    // [pieces][NQ * 128] (m, l)
-    int4* desc;         // [grid] unit left open by CTA c: (token, ntok, g, last CTA) or last = -1
-};
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                            int c1, int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
 template <int N>
 __device__ __forceinline__ void set_regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -115,303 +59,13 @@ template <int N>
 __device__ __forceinline__ void set_regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// 16 consecutive fp32 columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "{\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const float* v) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-    asm volatile(
-        "{\n\t"
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
-        "tcgen05.wait::st.sync.aligned;\n\t}"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// Request r: rows [a, a + n) of q, kv keys, all inside their buffers whatever the arrays say.
-struct Req { int a, n, kv; };
-__device__ __forceinline__ Req request(const PagedAttnArgs& p, int r) {
-    Req q;
-    q.a = min(max(__ldg(p.cu + r), 0), p.T);
-    q.n = min(max(__ldg(p.cu + r + 1), q.a), p.T) - q.a;
-    q.kv = min(max(__ldg(p.kv_lens + r), 0), p.table_width * p.ps);
-    return q;
-}
-__device__ __forceinline__ bool request_ok(const PagedAttnArgs& p, int r) {
-    const int a = __ldg(p.cu + r), b = __ldg(p.cu + r + 1), kv = __ldg(p.kv_lens + r);
-    return a >= 0 && b >= a && b <= p.T && kv >= 0 && kv <= p.table_width * p.ps;
-}
-
-// Visible keys of tokens [t, t + ntok) of a request, as [lo, hi]; key tiles touched.
-__device__ __forceinline__ void unit_keys(const Req& q, int t, int ntok, int swin, int* pos0, int* lo,
-                                          int* hi, int* nt) {
-    *pos0 = q.kv - q.n + t;
-    *hi = *pos0 + ntok - 1;                    // < kv
-    *lo = swin > 0 ? max(0, *pos0 - swin + 1) : 0;
-    *nt = *hi < 0 ? 0 : *hi / kTileKeys - *lo / kTileKeys + 1;
-}
-
-// A line of `total` places cut into `pieces` equal parts: the part that holds place x.
-__device__ __forceinline__ int owner_of(long long x, long long total, long long pieces) {
-    return (int)(((x + 1) * pieces - 1) / total);
-}
-
-// A unit's piece [u0, u1) of its nt + kUnitCost places (the last ones hold no key tile) as
-// key tiles.  False if it holds none and nothing is to be written for it.
-__device__ __forceinline__ bool piece_tiles(long long u0, long long u1, int cta, Piece& k) {
-    k.p0 = (int)min(u0, (long long)k.nt);
-    k.p1 = (int)min(u1, (long long)k.nt);
-    k.slot = k.p0 == 0 && k.p1 == k.nt ? -1 : 2 * cta + (k.p0 == 0 ? 1 : 0);
-    k.more = 1;
-    return k.p0 < k.p1 || (k.nt == 0 && u0 == 0);
-}
-
-// All keys: a CTA's piece [x, x1) of the line of (KV head, request, tile of tokens, key
-// tile).  Run by one warp.  start(): every CTA sums the costs of all requests by itself,
-// lanes over requests (over the tiles of tokens of a long one), from the lengths alone.
-struct WalkAll {
-    long long x, x1, u0, total, pieces;
-    long long unit_at;    // place of the piece's unit on the line
-    int head, r, qt;
-    bool whole;           // a unit is one place: nothing is cut
-    __device__ __forceinline__ int tile_cost(const PagedAttnArgs& p, const Req& q, int i, int tpu) const {
-        if (whole) return 1;
-        int pos0, lo, hi, nt;
-        unit_keys(q, i * tpu, min(tpu, q.n - i * tpu), p.swin, &pos0, &lo, &hi, &nt);
-        return nt + kUnitCost;
-    }
-    __device__ __forceinline__ static long long scan(long long v, int lane) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
-        }
-        return v;
-    }
-    // every lane's own request
-    __device__ __forceinline__ long long cost(const PagedAttnArgs& p, const Req& q, int tpu, int lane) const {
-        const int tiles = (q.n + tpu - 1) / tpu;
-        long long c = 0;
-        if (tiles <= 2)
-            for (int i = 0; i < tiles; ++i) c += tile_cost(p, q, i, tpu);
-        for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
-            const int src = __ffs(many) - 1;
-            const Req h{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.kv, src)};
-            long long sum = 0;
-            for (int i = lane; i < (h.n + tpu - 1) / tpu; i += 32) sum += tile_cost(p, h, i, tpu);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == src) c = sum;
-        }
-        return c;
-    }
-    // false: the lengths are not sound
-    __device__ __forceinline__ bool start(const Params& P, int tpu, int cta, int grid, int lane) {
-        const PagedAttnArgs& p = P.a;
-        const int per = (p.R + 31) / 32;
-        long long mine = 0, count = 0;
-        int most = 0;                       // costs of the most expensive unit
-        bool good = true;
-        whole = false;
-        auto load = [&](int i, int end) {
-            Req q{0, 0, 0};
-            if (i < end) q = request(p, i);
-            return q;
-        };
-        for (int s = 0; s < per; ++s) {
-            const int i = lane * per + s;
-            const Req q = load(i, p.R);
-            if (i < p.R) good &= request_ok(p, i);
-            mine += cost(p, q, tpu, lane);
-            const int last = (q.n + tpu - 1) / tpu - 1;
-            count += last + 1;
-            if (last >= 0)                  // (the last tile of tokens sees as many keys as any)
-                most = max(most, max(tile_cost(p, q, last, tpu), tile_cost(p, q, max(last - 1, 0), tpu)));
-        }
-        {
-            const long long units = __shfl_sync(0xffffffffu, scan(count, lane), 31) * p.hkv;
-            const long long line = __shfl_sync(0xffffffffu, scan(mine, lane), 31) * p.hkv;
-            most = __reduce_max_sync(0xffffffffu, most);
-            whole = (units + grid - 1) / grid * most <= (line + grid - 1) / grid + kMergeCost;
-            if (whole) mine = count;
-        }
-        const long long inc = scan(mine, lane);
-        const long long all = __shfl_sync(0xffffffffu, inc, 31);
-        total = all * p.hkv;
-        pieces = min((long long)grid, total);
-        x = x1 = u0 = 0;
-        head = r = qt = 0;
-        good = __all_sync(0xffffffffu, good);
-        if (cta >= pieces) return good;
-        x = cta * total / pieces;
-        x1 = (cta + 1) * total / pieces;
-        head = (int)(x / all);
-        long long off = x - head * all;      // in the head's part of the line
-        const unsigned holds = __ballot_sync(0xffffffffu, off < inc);
-        const int owner = __ffs(holds) - 1;
-        off -= __shfl_sync(0xffffffffu, inc - mine, owner);
-        const int end = min(p.R, (owner + 1) * per);
-        for (int base = owner * per;; base += 32) {          // the request
-            const long long c = cost(p, load(base + lane, end), tpu, lane), ci = scan(c, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                off -= __shfl_sync(0xffffffffu, ci - c, l);
-                r = base + l;
-                break;
-            }
-            off -= __shfl_sync(0xffffffffu, ci, 31);
-        }
-        const Req q = request(p, r);
-        for (int base = 0;; base += 32) {                    // its tile of tokens
-            const int i = base + lane;
-            const long long c = i * tpu < q.n ? tile_cost(p, q, i, tpu) : 0, ci = scan(c, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                off -= __shfl_sync(0xffffffffu, ci - c, l);
-                qt = base + l;
-                break;
-            }
-            off -= __shfl_sync(0xffffffffu, ci, 31);
-        }
-        u0 = off;
-        return good;
-    }
-    __device__ __forceinline__ bool next(const Params& P, int tpu, int cta, Piece& k) {
-        const PagedAttnArgs& p = P.a;
-        while (x < x1) {
-            Req q = request(p, r);
-            while ((long long)qt * tpu >= q.n) {
-                qt = 0;
-                if (++r == p.R) { r = 0; ++head; }
-                q = request(p, r);
-            }
-            const int t = qt * tpu;
-            k.ntok = min(tpu, q.n - t);
-            k.tok0 = q.a + t;
-            k.g = head;
-            k.r = r;
-            unit_keys(q, t, k.ntok, p.swin, &k.pos0, &k.lo, &k.hi, &k.nt);
-            k.tile0 = k.lo / kTileKeys;
-            const long long cost = whole ? 1 : k.nt + kUnitCost, from = u0, u1 = min(cost, u0 + (x1 - x));
-            unit_at = x - u0;
-            x += u1 - u0;
-            if (u1 == cost) { ++qt; u0 = 0; } else u0 = u1;
-            if (piece_tiles(from, whole ? k.nt : u1, cta, k)) return true;
-        }
-        return false;
-    }
-};
-
-// Selected blocks: whole units (KV head, token) round the CTAs, then the piece [x, x1) of
-// the line of the units left over.  Run by one warp, which compacts a unit's valid blocks
-// into the list.
-struct WalkSel {
-    long long unit, rounds_end, x, x1, total, pieces, unit_at;
-    __device__ __forceinline__ void start(const Params& P, int cta, int grid) {
-        const long long units = (long long)P.a.T * P.a.hkv;
-        unit = cta;
-        rounds_end = units - units % grid;
-        total = (units - rounds_end) * P.cost_sel;
-        pieces = min((long long)grid, total);
-        x = cta < pieces ? cta * total / pieces : 0;
-        x1 = cta < pieces ? (cta + 1) * total / pieces : 0;
-    }
-    __device__ __forceinline__ bool next(const Params& P, int cta, int grid, int lane, int* list, Piece& k) {
-        const PagedAttnArgs& p = P.a;
-        const int t_first = __ldg(p.cu), t_last = __ldg(p.cu + p.R);
-        for (;;) {
-            long long u, u0 = 0, u1 = P.cost_sel;
-            if (unit < rounds_end) {
-                u = unit;
-                unit += grid;
-            } else if (x < x1) {
-                const long long i = x / P.cost_sel;
-                u0 = x - i * P.cost_sel;
-                u1 = min(u1, u0 + (x1 - x));
-                u = rounds_end + i;
-                unit_at = x - u0;
-                x += u1 - u0;
-            } else {
-                return false;
-            }
-            const int g = (int)(u / p.T), t = (int)(u - (long long)g * p.T);
-            if (t < t_first || t >= t_last) continue;
-            const int32_t* row = p.bidx + ((long long)t * p.hkv + g) * p.topk;
-            const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
-            const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
-            k.r = seq_of_token(p.cu, p.R, t);
-            const Req q = request(p, k.r);
-            if (t < q.a || t >= q.a + q.n) continue;
-            int nt;
-            unit_keys(q, t - q.a, 1, p.swin, &k.pos0, &k.lo, &k.hi, &nt);
-            const int pos = k.pos0, qb = pos >= 0 ? pos / p.bs : -1;
-            const unsigned m0 = __ballot_sync(0xffffffffu, block_valid(b0, qb, pos, p.bs, p.swin));
-            const unsigned m1 = __ballot_sync(0xffffffffu, block_valid(b1, qb, pos, p.bs, p.swin));
-            const unsigned below = (1u << lane) - 1u;
-            if (m0 >> lane & 1) list[__popc(m0 & below)] = b0;
-            if (m1 >> lane & 1) list[__popc(m0) + __popc(m1 & below)] = b1;
-            __syncwarp();
-            k.nb = __popc(m0) + __popc(m1);
-            k.tok0 = t;
-            k.ntok = 1;
-            k.g = g;
-            const int per = kTileKeys / p.bs;
-            k.nt = (k.nb + per - 1) / per;
-            if (piece_tiles(u0, u1, cta, k)) return true;
-        }
-    }
-};
-
-// The visible columns of key tile j of a piece, as two inclusive ranges: columns
-// [l0, h0] of the first 64 and [l1, h1] of the last 64 (empty: l > h).  For the unit as a
-// whole; rows narrow them further.
-template <bool SEL>
-__device__ __forceinline__ void tile_cols(const Params& P, const Piece& k, const int* list, int j, int& l0,
-                                          int& h0, int& l1, int& h1) {
-    if (!SEL) {
-        const int key0 = (k.tile0 + j) * kTileKeys;
-        l0 = max(k.lo - key0, 0);
-        h1 = min(k.hi - key0, 127);
-        h0 = min(h1, 63);
-        l1 = max(l0, 64);
-    } else if (P.a.bs == 128) {
-        const int key0 = list[j] * 128;
-        l0 = max(k.lo - key0, 0);
-        h1 = min(k.hi - key0, 127);
-        h0 = min(h1, 63);
-        l1 = max(l0, 64);
-    } else {
-        const int key0 = list[2 * j] * 64;
-        l0 = max(k.lo - key0, 0);
-        h0 = min(k.hi - key0, 63);
-        l1 = 128;
-        h1 = -1;
-        if (2 * j + 1 < k.nb) {
-            const int key1 = list[2 * j + 1] * 64;
-            l1 = 64 + max(k.lo - key1, 0);
-            h1 = 64 + min(k.hi - key1, 63);
-        }
-    }
-}
-
 template <int F16, int D, int NQ, bool SEL>
 __global__ void __launch_bounds__(kPaThreads, 1)
     k_paged_attn(const Params P, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using Smem = PaSmem<D>;
     constexpr int kHalves = Smem::kHalves, kStages = Smem::kStages;
-    constexpr int kAhead = NQ == 2 ? 1 : 2;       // K tiles loaded and multiplied ahead of V
+    using Stages = Ring<3 - NQ, kStages / (3 - NQ), 1>;
     extern __shared__ uint8_t smem_raw[];
     Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const PagedAttnArgs& p = P.a;
@@ -420,7 +74,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = (tid >> 5) < 4 ? kSoftmaxWarps + (tid >> 5) : (tid >> 5) - 4;
     const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
-    const int tpu = NQ * P.tpt;
 
     if (tid == 0) {
         S.abort_flag = 0;
@@ -462,149 +115,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
-    volatile int* abort_flag = &S.abort_flag;
-    // Bounded wait of a whole warp; false in every lane if any lane gave up.
-    auto wait_lane = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (*abort_flag) return false;
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long start = clock64();
-#pragma unroll 1
-        while (!mbar_try_wait(bar, parity)) {
-            if (clock64() - start > kWaitBudgetCycles) {
-                S.err = NSA_ERR_TIMEOUT;
-                *abort_flag = 1;
-                return false;
-            }
-        }
-        return true;
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_lane(bar, parity));
-    };
-    // piece i of the ring, once it is there; release(i): this warp is done with it
-    auto fetch = [&](int i) -> bool { return wait(&S.ring_full[i % kRing], (i / kRing) & 1); };
-    auto release = [&](int i) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.ring_empty[i % kRing]);
-    };
+    const Waiter wait{&S.abort_flag, &S.err};
+    auto fetch = [&](int i) -> bool { return fetch_piece(S, wait, i); };
+    auto release = [&](int i) { release_piece(S, lane, i); };
 
     // setmaxnreg at the head of each role: the compiler gives the code behind it that many
     if (warp >= kSoftmaxWarps) {
         set_regs_dec<kOtherRegs>();
     if (warp == 8) {
-        // ------------------------------------------------------------- TMA producer
-        const int boxes = kTileKeys / P.box_rows;      // per tile and 64-column half
-        const int box = lane / kHalves, half = lane - box * kHalves;
-        const uint32_t box_bytes = (uint32_t)P.box_rows * 128u;
-        // Place n of the stage ring: K tiles at 0 and 2 t - 1 (NQ = 1) or 2 t (NQ = 2), V
-        // tiles at 2 t + 2 or 2 t + 1: the order of use, K K V K V K V .. or K V K V ..
-        int n = 0;
-        int units = 0;              // units whose Q was loaded
-        int at = -1;                // piece being loaded
-        int j = 0, j_end = 0;       // its next key tile
-        // the tiles whose K is on its way and whose V is not
-        int page_q[kAhead] = {}, row_q[kAhead] = {}, g_q[kAhead] = {};
-        unsigned mask_q[kAhead] = {};
-        int pending = 0;
-        bool ok = true, more = true;
-        auto load = [&](const CUtensorMap* map, int page, int row, int g, unsigned mask) -> bool {
-            const int stg = n % kStages;
-            if (!wait(&S.kv_empty[stg], ((n / kStages) & 1) ^ 1)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[stg], (uint32_t)__popc(mask) * box_bytes);
-            __syncwarp();
-            if (mask >> lane & 1)
-                tma_load_4d(S.kv[stg][half] + box * box_bytes, map, &S.kv_full[stg], half * 64, g, row, page);
-            ++n;
-            return true;
-        };
-        while (ok) {
-            while (more && j == j_end) {          // the next piece with a key tile
-                if (at >= 0) release(at);
-                ++at;
-                if (!(ok = fetch(at))) break;
-                const Piece& k = S.ring[at % kRing];
-                more = k.more != 0;
-                j = k.p0;
-                j_end = k.p1;
-                if (!more || j == j_end) continue;
-                const int qb = NQ == 2 ? 0 : units & 1;
-                const int use = NQ == 2 ? units : units >> 1;
-                if (!(ok = wait(&S.q_empty[qb], (use & 1) ^ 1))) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&S.q_full[qb], (uint32_t)(NQ * kHalves * P.tpt * p.G) * 128u);
-                __syncwarp();
-                if (lane < NQ * kHalves) {
-                    const int tile = lane / kHalves, hf = lane - tile * kHalves;
-                    tma_load_3d(S.q[NQ == 2 ? tile : qb][hf], &qmap, &S.q_full[qb], hf * 64, k.g * p.G,
-                                k.tok0 + tile * P.tpt);
-                }
-                ++units;
-            }
-            if (!ok) break;
-            if (more) {
-                // this lane's box of key tile j: the page, the row in it, and whether a
-                // visible key lies in it
-                const Piece& k = S.ring[at % kRing];
-                const int c0 = box * P.box_rows;
-                int key = -1;
-                if (lane < boxes * kHalves) {
-                    if (!SEL) {
-                        key = (k.tile0 + j) * kTileKeys + c0;
-                    } else {
-                        const int e = j * (kTileKeys / p.bs) + c0 / p.bs;
-                        if (e < k.nb) key = S.list[at % kRing][e] * p.bs + c0 % p.bs;
-                    }
-                }
-                const bool live = key >= 0 && key <= k.hi && key + P.box_rows > k.lo;
-                int page = 0, row = 0;
-                if (live) {
-                    page = __ldg(p.table + (long long)k.r * p.table_stride + key / p.ps);
-                    row = key % p.ps;
-                    if (page < 0 || page >= p.num_pages) {   // reads as zeros
-                        S.err = NSA_ERR_BAD_INDEX;
-                        page = p.num_pages;
-                    }
-                }
-                const unsigned mask = __ballot_sync(0xffffffffu, live);
-                const int g = k.g;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    if (i == pending) {
-                        page_q[i] = page;
-                        row_q[i] = row;
-                        g_q[i] = g;
-                        mask_q[i] = mask;
-                    }
-                if (!(ok = load(&kmap, page, row, g, mask))) break;
-                ++pending;
-                ++j;
-                if (pending < kAhead) continue;
-            } else if (NQ == 1) {
-                ++n;                // no K tile is left for this place
-            }
-            if (pending == 0) break;
-            if (!(ok = load(&vmap, page_q[0], row_q[0], g_q[0], mask_q[0]))) break;
-#pragma unroll
-            for (int i = 0; i + 1 < kAhead; ++i) {
-                page_q[i] = page_q[i + 1];
-                row_q[i] = row_q[i + 1];
-                g_q[i] = g_q[i + 1];
-                mask_q[i] = mask_q[i + 1];
-            }
-            --pending;
-        }
-        if (*abort_flag && lane == 0) {   // let copies still in flight land before the CTA exits
-            const long long start = clock64();
-            auto land = [&](uint64_t* bar, uint32_t parity) {
-                while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitBudgetCycles) {}
-            };
-            for (int i = 0; i < 2; ++i) {
-                const int uses = NQ == 2 ? (i == 0 ? units : 0) : (units + 1 - i) / 2;
-                if (uses > 0) land(&S.q_full[i], (uses - 1) & 1);
-            }
-            for (int i = max(n - kStages, 0); i < n; ++i) land(&S.kv_full[i % kStages], (i / kStages) & 1);
-        }
-        __syncwarp();
+        produce<SEL, NQ, Stages>(S, P, wait, &qmap, &kmap, &vmap, lane);
     } else if (warp != 10) {
         // ------------------------------------------------------------- MMA issuers
         // Warp 9 issues for stream 0, warp 11 for stream 1.  A stream's next S follows its
@@ -635,7 +154,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         int count_s = 0, count_o = 0;     // key tiles of the pieces so far, both streams
         bool rows_s = true, rows_o = true;   // the unit has rows in this stream's tile
         int qb = 0;
-        bool head_s = false, first_o = true;
+        bool first_o = true;
         int lo_o = 0, hi_o = 0, tile0_o = 0;
         int sums = 0, items = 0;          // sums completed, P V items
         bool ok = true, more_s = true, more_o = true;
@@ -655,20 +174,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 base_s = count_s - p0;
                 count_s += nt;
                 rows_s = NQ == 1 || st == 0 || k.ntok > P.tpt;
-                head_s = true;
-                if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);   // no tile for this stream
-            }
-            if (!more_s) return true;
-            if (head_s) {
+                // (a unit without a tile for this stream is waited for as well, or this
+                // issuer could be done with a later Q of the buffer before the other is with
+                // this one)
                 const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
                 if (!wait(&S.q_full[qb], use & 1)) return false;
-                head_s = false;
+                if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
             }
-            const int t = base_s + js, n = NQ == 2 ? 2 * t : max(2 * t - 1, 0);
-            return wait(&S.kv_full[n % kStages], (n / kStages) & 1);
+            if (!more_s) return true;
+            const auto to = Stages::k(base_s + js);
+            return wait(&S.kv_full[to.stage], to.phase);
         };
         auto issue_s = [&]() {
-            const int t = base_s + js, stg = (NQ == 2 ? 2 * t : max(2 * t - 1, 0)) % kStages;
+            const int stg = Stages::k(base_s + js).stage;
             const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? st : qb) * kTileU);
             const uint32_t b0 = u(k_desc0 + (uint32_t)stg * kTileU);
             if (rows_s) {
@@ -704,8 +222,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 first_o = true;
             }
             if (!ok || !more_o) break;
-            const int t = base_o + jo, n = NQ == 2 ? 2 * t + 1 : 2 * t + 2, stg = n % kStages;
-            if (!(ok = wait(&S.kv_full[stg], (n / kStages) & 1))) break;
+            const auto from = Stages::v(base_o + jo);
+            const int stg = from.stage;
+            if (!(ok = wait(&S.kv_full[stg], from.phase))) break;
             // the tile's visible columns; all of them but at a piece's ends
             int l0, h0, l1, h1;
             if (SEL) {
@@ -776,39 +295,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             while (!mbar_try_wait(&S.drain, 0) && clock64() - start < kWaitBudgetCycles) {}
         }
     } else {
-        // --------------------------------------------------------------- scheduler
-        WalkAll wall{};
-        WalkSel wsel{};
-        if (SEL) {
-            wsel.start(P, cta, grid);
-            bool good = true;
-            if (cta == 0)
-                for (int r = lane; r < p.R; r += 32) good &= request_ok(p, r);
-            if (!good) S.err = NSA_ERR_BAD_INDEX;
-        } else if (!wall.start(P, tpu, cta, grid, lane)) {
-            S.err = NSA_ERR_BAD_INDEX;
-        }
-        // the unit this CTA starts and leaves open, for the merge, and who finishes it
-        int4 open = make_int4(0, 0, 0, -1);
-        for (int i = 0;; ++i) {
-            const int at = i % kRing;
-            if (!wait(&S.ring_empty[at], ((i / kRing) & 1) ^ 1)) break;
-            Piece k{};
-            if (SEL) {
-                if (!wsel.next(P, cta, grid, lane, S.list[at], k)) k.more = 0;
-            } else {
-                if (!wall.next(P, tpu, cta, k)) k.more = 0;
-            }
-            if (k.more && k.slot == 2 * cta + 1)     // its last key tile's place on the line
-                open = make_int4(k.tok0, k.ntok, k.g,
-                                 SEL ? owner_of(wsel.unit_at + k.nt - 1, wsel.total, wsel.pieces)
-                                     : owner_of(wall.unit_at + k.nt - 1, wall.total, wall.pieces));
-            if (lane == 0) S.ring[at] = k;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.ring_full[at]);
-            if (!k.more) break;
-        }
-        if (lane == 0) P.desc[cta] = open;
+        schedule<SEL>(S, P, wait, P.tpu, cta, grid, lane);
     }
     } else {
         set_regs_inc<kSoftmaxRegs>();
@@ -1011,14 +498,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 8) tmem_dealloc(tmem, 512);
-    if (tid == 0) {
-        // one status byte per CTA, always written: nothing has to be cleared before the call
-        p.st->cta_err[cta] = (unsigned char)S.err;
-        if (cta == 0) {
-            p.st->code = 0;
-            for (int i = grid; i < kMaxStatusCtas; ++i) p.st->cta_err[i] = 0;
-        }
-    }
+    if (tid == 0) finish_status(p.st, S.err, cta, grid);
 }
 
 // Joins the partial results of the unit that CTA blockIdx.x left open, in the order of the
@@ -1105,13 +585,14 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     k_paged_attn<F16, D, NQ, SEL><<<grid, kPaThreads, smem, stream>>>(P, qmap, kmap, vmap);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // nothing is cut where whole units fill the rounds
-    if (SEL && (long long)P.a.T * P.a.hkv % grid == 0) return cudaSuccess;
-    // The merge is launched while the attention kernel still runs and waits for its end
-    // (programmatic dependent launch): its launch costs nothing then.
+    return cudaGetLastError();
+}
+
+// The merge is launched while the attention kernel still runs and waits for its end
+// (programmatic dependent launch): its launch costs nothing then.
+cudaError_t merge(const Params& P, int f16, int grid, int rows_per_piece, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(NQ * 4, (P.a.G * (SEL ? 1 : NQ * P.tpt) + 7) / 8));
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(rows_per_piece / 32, (P.a.G * P.tpu + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -1119,7 +600,9 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_merge<F16, D>, P, NQ * 128);
+    auto* kernel = P.a.d == 64 ? (f16 ? k_paged_merge<1, 64> : k_paged_merge<0, 64>)
+                               : (f16 ? k_paged_merge<1, 128> : k_paged_merge<0, 128>);
+    return cudaLaunchKernelEx(&cfg, kernel, P, rows_per_piece);
 }
 
 template <int F16, int D>
@@ -1133,6 +616,13 @@ cudaError_t dispatch(const Params& P, bool two, int grid, const CUtensorMap& q, 
 // Two tiles of query rows per unit where the batch has more than one tile of rows per
 // request and KV head on average.
 bool two_tiles(const PagedAttnArgs& p) { return (long long)p.T * p.G > 128ll * p.R; }
+
+// Units of few query rows take the transposed products: at most 16 or 32 rows of a token's
+// query heads (selected blocks), or on average over the requests' new tokens.
+int few_rows(const PagedAttnArgs& p) {
+    const long long rows = p.bidx ? p.G : std::max<long long>(p.G, (long long)p.T * p.G / p.R);
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+}
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -1155,7 +645,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     P.part_ml = reinterpret_cast<float2*>(ws);
     P.part_o = reinterpret_cast<float*>(ws + align256(pieces * 256 * sizeof(float2)));
     const bool sel = a.bidx != nullptr;
-    P.tpt = sel ? 1 : kTileRows / a.G;
+    const int few = few_rows(a);
+    const bool two = !few && !sel && two_tiles(a);
+    P.tpt = sel ? 1 : (few ? few : kTileRows) / a.G;
+    P.tpu = two ? 2 * P.tpt : P.tpt;
     P.box_rows = std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys);
     int grid = std::min(num_sms, kMaxStatusCtas);
     if (sel) {
@@ -1178,12 +671,19 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     if (!encode(&qmap, f16, 3, a.q, qdims, qstr, qbox) || !encode(&kmap, f16, 4, a.k, kdims, kstr, kbox) ||
         !encode(&vmap, f16, 4, a.v, kdims, kstr, kbox))
         return cudaErrorInvalidValue;
-    const bool two = !sel && two_tiles(a);
-    if (a.d == 64)
-        return f16 ? dispatch<1, 64>(P, two, grid, qmap, kmap, vmap, stream)
-                   : dispatch<0, 64>(P, two, grid, qmap, kmap, vmap, stream);
-    return f16 ? dispatch<1, 128>(P, two, grid, qmap, kmap, vmap, stream)
-               : dispatch<0, 128>(P, two, grid, qmap, kmap, vmap, stream);
+    cudaError_t e;
+    if (few)
+        e = launch_paged_few(P, f16, few, grid, qmap, kmap, vmap, stream);
+    else if (a.d == 64)
+        e = f16 ? dispatch<1, 64>(P, two, grid, qmap, kmap, vmap, stream)
+                : dispatch<0, 64>(P, two, grid, qmap, kmap, vmap, stream);
+    else
+        e = f16 ? dispatch<1, 128>(P, two, grid, qmap, kmap, vmap, stream)
+                : dispatch<0, 128>(P, two, grid, qmap, kmap, vmap, stream);
+    if (e != cudaSuccess) return e;
+    // nothing is cut where whole units fill the rounds
+    if (sel && (long long)a.T * a.hkv % grid == 0) return cudaSuccess;
+    return merge(P, f16, grid, two ? 256 : 128, stream);
 }
 
 }  // namespace nsa

@@ -124,6 +124,26 @@ def test_attend_one_long_request_is_split():
     run(make_case([2], [9000], 8, 8, 64, 128, seed=12, window=8000))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_len, group", [(1, 1), (1, 16), (5, 4), (1, 32), (11, 8)])
+def test_attend_many_tiles_per_block(q_len, group, d):
+    # long runs of key tiles and several units on every SM: the rings of stages, the buffers
+    # and their barriers go round many times
+    hkv, R = 8, 24
+    rng = np.random.default_rng(q_len + group)
+    kv = rng.integers(2500, 6000, R)
+    kv[:5] = [300, 129, 128, 127, 11]
+    run(make_case([q_len] * R, kv.tolist(), group * hkv, hkv, d, 64, seed=30 + group, poison=False))
+
+
+@pytest.mark.parametrize("hq, hkv, q_lens", [(4, 4, [1] * 150), (32, 8, [3, 1, 2, 5] * 30), (64, 4, [1, 2] * 60)])
+def test_attend_many_units_of_one_tile(hq, hkv, q_lens):
+    # a unit's only key tile is now one stream's, now the other's
+    kv = [n + (37 * i) % 120 for i, n in enumerate(q_lens)]
+    for seed in range(3):
+        run(make_case(q_lens, kv, hq, hkv, 128, 16, seed=40 + seed))
+
+
 # ------------------------------------------------------------------------ selected blocks
 
 @pytest.mark.parametrize("bs", [64, 128])
@@ -165,6 +185,15 @@ def test_select_all_blocks_equals_attend():
 
 def test_select_many_tokens():
     run(make_case([300, 211], [2000, 211], 16, 4, 128, 64, seed=15, topk=8, pad=3))
+
+
+@pytest.mark.parametrize("hq, hkv, topk", [(8, 4, 2), (64, 2, 1), (80, 2, 3), (16, 8, 16)])
+def test_select_many_units(hq, hkv, topk):
+    rng = np.random.default_rng(hq)
+    kv = rng.integers(1, 1500, 160)
+    q = np.minimum(kv, rng.integers(0, 4, 160))
+    for seed in range(2):
+        run(make_case(q.tolist(), kv.tolist(), hq, hkv, 128, 64, seed=50 + seed, topk=topk, pad=1))
 
 
 # ------------------------------------------------------- layouts, streams, graphs, status
