@@ -617,11 +617,14 @@ cudaError_t dispatch(const Params& P, bool two, int grid, const CUtensorMap& q, 
 // request and KV head on average.
 bool two_tiles(const PagedAttnArgs& p) { return (long long)p.T * p.G > 128ll * p.R; }
 
-// Units of few query rows take the transposed products: at most 16 or 32 rows of a token's
-// query heads (selected blocks), or on average over the requests' new tokens.
-int few_rows(const PagedAttnArgs& p) {
-    const long long rows = p.bidx ? p.G : std::max<long long>(p.G, (long long)p.T * p.G / p.R);
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+// The transposed products for units of few query rows: up to kFewRows rows of a token's query
+// heads (selected blocks), or of a request's new tokens on average.  Measured against tiles of
+// 128 rows: 64 requests of one token, 4 rows a unit, 637 against 685 us; 8 rows, 16 selected
+// blocks, 68 against 71 us, a chunk of 512 such tokens 322 against 390 us.  The same kernel
+// with 32 rows lost (16 requests of 3 - 9 tokens, 24 rows on average: 92 against 66 us): its
+// Q and P^T leave room for two thirds of the K / V stages only.
+bool few_rows(const PagedAttnArgs& p) {
+    return (p.bidx ? p.G : std::max<long long>(p.G, (long long)p.T * p.G / p.R)) <= kFewRows;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -645,9 +648,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     P.part_ml = reinterpret_cast<float2*>(ws);
     P.part_o = reinterpret_cast<float*>(ws + align256(pieces * 256 * sizeof(float2)));
     const bool sel = a.bidx != nullptr;
-    const int few = few_rows(a);
+    const bool few = few_rows(a);
     const bool two = !few && !sel && two_tiles(a);
-    P.tpt = sel ? 1 : (few ? few : kTileRows) / a.G;
+    P.tpt = sel ? 1 : (few ? kFewRows : kTileRows) / a.G;
     P.tpu = two ? 2 * P.tpt : P.tpt;
     P.box_rows = std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys);
     int grid = std::min(num_sms, kMaxStatusCtas);
@@ -673,7 +676,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (few)
-        e = launch_paged_few(P, f16, few, grid, qmap, kmap, vmap, stream);
+        e = launch_paged_few(P, f16, grid, qmap, kmap, vmap, stream);
     else if (a.d == 64)
         e = f16 ? dispatch<1, 64>(P, two, grid, qmap, kmap, vmap, stream)
                 : dispatch<0, 64>(P, two, grid, qmap, kmap, vmap, stream);

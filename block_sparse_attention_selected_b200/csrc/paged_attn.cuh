@@ -111,8 +111,11 @@ __device__ __forceinline__ void unit_keys(const Req& q, int t, int ntok, int swi
 }
 
 // A line of `total` places cut into `pieces` equal parts: the part that holds place x.
+__device__ __forceinline__ long long quotient(long long a, long long b) {   // of a, b >= 0
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ int owner_of(long long x, long long total, long long pieces) {
-    return (int)(((x + 1) * pieces - 1) / total);
+    return (int)quotient((x + 1) * pieces - 1, total);
 }
 
 // A unit's piece [u0, u1) of its nt + kUnitCost places (the last ones hold no key tile) as
@@ -168,7 +171,8 @@ struct WalkAll {
     __device__ __forceinline__ bool start(const Params& P, int tpu, int cta, int grid, int lane) {
         const PagedAttnArgs& p = P.a;
         const int per = (p.R + 31) / 32;
-        long long mine = 0, count = 0;
+        long long mine = 0;
+        int count = 0;
         int most = 0;                       // costs of the most expensive unit
         bool good = true;
         whole = false;
@@ -187,42 +191,49 @@ struct WalkAll {
             if (last >= 0)                  // (the last tile of tokens sees as many keys as any)
                 most = max(most, max(tile_cost(p, q, last, tpu), tile_cost(p, q, max(last - 1, 0), tpu)));
         }
+        long long inc = scan(mine, lane);
+        long long all = __shfl_sync(0xffffffffu, inc, 31);
         {
-            const long long units = __shfl_sync(0xffffffffu, scan(count, lane), 31) * p.hkv;
-            const long long line = __shfl_sync(0xffffffffu, scan(mine, lane), 31) * p.hkv;
+            // (units of one KV head: at most total_tokens)
+            const long long units = (long long)__reduce_add_sync(0xffffffffu, count) * p.hkv;
             most = __reduce_max_sync(0xffffffffu, most);
-            whole = (units + grid - 1) / grid * most <= (line + grid - 1) / grid + kMergeCost;
-            if (whole) mine = count;
+            whole = quotient(units + grid - 1, grid) * most <= quotient(all * p.hkv + grid - 1, grid) + kMergeCost;
+            if (whole) {
+                mine = count;
+                inc = scan(mine, lane);
+                all = __shfl_sync(0xffffffffu, inc, 31);
+            }
         }
-        const long long inc = scan(mine, lane);
-        const long long all = __shfl_sync(0xffffffffu, inc, 31);
         total = all * p.hkv;
         pieces = min((long long)grid, total);
         x = x1 = u0 = 0;
         head = r = qt = 0;
         good = __all_sync(0xffffffffu, good);
         if (cta >= pieces) return good;
-        x = cta * total / pieces;
-        x1 = (cta + 1) * total / pieces;
-        head = (int)(x / all);
+        x = quotient(cta * total, pieces);
+        x1 = quotient((cta + 1) * total, pieces);
+        head = (int)quotient(x, all);
         long long off = x - head * all;      // in the head's part of the line
         const unsigned holds = __ballot_sync(0xffffffffu, off < inc);
         const int owner = __ffs(holds) - 1;
         off -= __shfl_sync(0xffffffffu, inc - mine, owner);
-        const int end = min(p.R, (owner + 1) * per);
-        for (int base = owner * per;; base += 32) {          // the request
-            const long long c = cost(p, load(base + lane, end), tpu, lane), ci = scan(c, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                off -= __shfl_sync(0xffffffffu, ci - c, l);
-                r = base + l;
-                break;
+        r = owner * per;
+        if (per > 1) {                       // the request, among the owner's
+            const int end = min(p.R, (owner + 1) * per);
+            for (int base = r;; base += 32) {
+                const long long c = cost(p, load(base + lane, end), tpu, lane), ci = scan(c, lane);
+                const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
+                if (hit) {
+                    const int l = __ffs(hit) - 1;
+                    off -= __shfl_sync(0xffffffffu, ci - c, l);
+                    r = base + l;
+                    break;
+                }
+                off -= __shfl_sync(0xffffffffu, ci, 31);
             }
-            off -= __shfl_sync(0xffffffffu, ci, 31);
         }
         const Req q = request(p, r);
-        for (int base = 0;; base += 32) {                    // its tile of tokens
+        for (int base = 0; q.n > tpu; base += 32) {          // its tile of tokens
             const int i = base + lane;
             const long long c = i * tpu < q.n ? tile_cost(p, q, i, tpu) : 0, ci = scan(c, lane);
             const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
@@ -263,6 +274,21 @@ struct WalkAll {
     }
 };
 
+// The last request with cu[r] <= t, by one warp: two rounds of loads for up to 1024 requests.
+__device__ __forceinline__ int find_request(const PagedAttnArgs& p, int t, int lane) {
+    const int step = (p.R + 31) / 32, i = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i < p.R && __ldg(p.cu + i) <= t);
+    int r = (31 - __clz(m | 1u)) * step;
+    if (step == 1) return r;
+    const int end = min(r + step, p.R);
+    for (int base = r; base < end; base += 32) {
+        const unsigned b = __ballot_sync(0xffffffffu, base + lane < end && __ldg(p.cu + base + lane) <= t);
+        if (b) r = base + 31 - __clz(b);
+        if (b != 0xffffffffu) break;
+    }
+    return r;
+}
+
 // Selected blocks: whole units (KV head, token) round the CTAs, then the piece [x, x1) of
 // the line of the units left over.  Run by one warp, which compacts a unit's valid blocks
 // into the list.
@@ -274,8 +300,8 @@ struct WalkSel {
         rounds_end = units - units % grid;
         total = (units - rounds_end) * P.cost_sel;
         pieces = min((long long)grid, total);
-        x = cta < pieces ? cta * total / pieces : 0;
-        x1 = cta < pieces ? (cta + 1) * total / pieces : 0;
+        x = cta < pieces ? quotient(cta * total, pieces) : 0;
+        x1 = cta < pieces ? quotient((cta + 1) * total, pieces) : 0;
     }
     __device__ __forceinline__ bool next(const Params& P, int cta, int grid, int lane, int* list, Piece& k) {
         const PagedAttnArgs& p = P.a;
@@ -286,7 +312,7 @@ struct WalkSel {
                 u = unit;
                 unit += grid;
             } else if (x < x1) {
-                const long long i = x / P.cost_sel;
+                const long long i = quotient(x, P.cost_sel);
                 u0 = x - i * P.cost_sel;
                 u1 = min(u1, u0 + (x1 - x));
                 u = rounds_end + i;
@@ -295,12 +321,12 @@ struct WalkSel {
             } else {
                 return false;
             }
-            const int g = (int)(u / p.T), t = (int)(u - (long long)g * p.T);
+            const int g = (int)quotient(u, p.T), t = (int)(u - (long long)g * p.T);
             if (t < t_first || t >= t_last) continue;
             const int32_t* row = p.bidx + ((long long)t * p.hkv + g) * p.topk;
             const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
             const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
-            k.r = seq_of_token(p.cu, p.R, t);
+            k.r = find_request(p, t, lane);
             const Req q = request(p, k.r);
             if (t < q.a || t >= q.a + q.n) continue;
             int nt;
@@ -471,15 +497,50 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
     const int boxes = kTileKeys / P.box_rows;      // per tile and 64-column half
     const int box = lane / kHalves, half = lane - box * kHalves;
     const uint32_t box_bytes = (uint32_t)P.box_rows * 128u;
+    // (page and block sizes are powers of two)
+    const int ps_log2 = 31 - __clz(p.ps), bs_log2 = SEL ? 31 - __clz(p.bs) : 0;
+    const int c0 = box * P.box_rows;               // this lane's box: its first key in the tile
     int tk = 0, tv = 0;         // K and V tiles loaded
     int units = 0;              // units whose Q was loaded
-    int at = -1;                // piece being loaded
-    int j = 0, j_end = 0;       // its next key tile
+    int at = -1;                // piece of the next K tile
+    int j = 0, j_end = 0;       // the key tile after it
+    bool ok = true, more = true, new_unit = false;
+    // The next K tile's box of this lane.  It is looked up one tile ahead: the block table's
+    // entry comes from L2 or memory, and would hold up every tile.
+    bool nx_live = false;
+    int nx_page = 0, nx_row = 0, nx_g = 0;
+    auto advance = [&]() -> bool {
+        while (more && j == j_end) {          // the next piece with a key tile
+            if (at >= 0) release_piece(S, lane, at);
+            if (!fetch_piece(S, wait, ++at)) return false;
+            const Piece& k = S.ring[at % kRing];
+            more = k.more != 0;
+            j = k.p0;
+            j_end = k.p1;
+            new_unit = true;
+        }
+        if (!more) return true;
+        const Piece& k = S.ring[at % kRing];
+        int key = -1;
+        if (lane < boxes * kHalves) {
+            if (!SEL) {
+                key = (k.tile0 + j) * kTileKeys + c0;
+            } else {
+                const int e = ((j * kTileKeys) >> bs_log2) + (c0 >> bs_log2);
+                if (e < k.nb) key = (S.list[at % kRing][e] << bs_log2) + (c0 & (p.bs - 1));
+            }
+        }
+        nx_live = key >= 0 && key <= k.hi && key + P.box_rows > k.lo;   // a visible key lies in it
+        nx_row = key & (p.ps - 1);
+        nx_g = k.g;
+        if (nx_live) nx_page = __ldg(p.table + (long long)k.r * p.table_stride + (key >> ps_log2));
+        ++j;
+        return true;
+    };
     // the tiles whose K is on its way and whose V is not
     int page_q[kRun] = {}, row_q[kRun] = {}, g_q[kRun] = {};
     unsigned mask_q[kRun] = {};
     int pending = 0;
-    bool ok = true, more = true;
     auto load = [&](const CUtensorMap* map, typename Stages::At to, int page, int row, int g, unsigned mask) -> bool {
         const int stg = to.stage;
         if (!wait(&S.kv_empty[stg], to.phase ^ 1)) return false;
@@ -489,68 +550,42 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
             tma_load_4d(S.kv[stg][half] + box * box_bytes, map, &S.kv_full[stg], half * 64, g, row, page);
         return true;
     };
+    ok = advance();
     while (ok) {
-        while (more && j == j_end) {          // the next piece with a key tile
-            if (at >= 0) release_piece(S, lane, at);
-            ++at;
-            if (!(ok = fetch_piece(S, wait, at))) break;
-            const Piece& k = S.ring[at % kRing];
-            more = k.more != 0;
-            j = k.p0;
-            j_end = k.p1;
-            if (!more || j == j_end) continue;
-            const int qb = kTiles == 2 ? 0 : units & 1;
-            const int use = kTiles == 2 ? units : units >> 1;
-            if (!(ok = wait(&S.q_empty[qb], (use & 1) ^ 1))) break;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&S.q_full[qb], (uint32_t)(kTiles * kHalves * P.tpt * p.G) * 128u);
-            __syncwarp();
-            if (lane < kTiles * kHalves) {
-                const int tile = lane / kHalves, hf = lane - tile * kHalves;
-                tma_load_3d(S.q[kTiles == 2 ? tile : qb][hf], qmap, &S.q_full[qb], hf * 64, k.g * p.G,
-                            k.tok0 + tile * P.tpt);
-            }
-            ++units;
-        }
-        if (!ok) break;
         if (more) {
-            // this lane's box of key tile j: the page, the row in it, and whether a
-            // visible key lies in it
-            const Piece& k = S.ring[at % kRing];
-            const int c0 = box * P.box_rows;
-            int key = -1;
-            if (lane < boxes * kHalves) {
-                if (!SEL) {
-                    key = (k.tile0 + j) * kTileKeys + c0;
-                } else {
-                    const int e = j * (kTileKeys / p.bs) + c0 / p.bs;
-                    if (e < k.nb) key = S.list[at % kRing][e] * p.bs + c0 % p.bs;
+            if (new_unit) {
+                const Piece& k = S.ring[at % kRing];
+                const int qb = kTiles == 2 ? 0 : units & 1;
+                const int use = kTiles == 2 ? units : units >> 1;
+                if (!(ok = wait(&S.q_empty[qb], (use & 1) ^ 1))) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&S.q_full[qb], (uint32_t)(kTiles * kHalves * P.tpt * p.G) * 128u);
+                __syncwarp();
+                if (lane < kTiles * kHalves) {
+                    const int tile = lane / kHalves, hf = lane - tile * kHalves;
+                    tma_load_3d(S.q[kTiles == 2 ? tile : qb][hf], qmap, &S.q_full[qb], hf * 64, k.g * p.G,
+                                k.tok0 + tile * P.tpt);
                 }
+                ++units;
+                new_unit = false;
             }
-            const bool live = key >= 0 && key <= k.hi && key + P.box_rows > k.lo;
-            int page = 0, row = 0;
-            if (live) {
-                page = __ldg(p.table + (long long)k.r * p.table_stride + key / p.ps);
-                row = key % p.ps;
-                if (page < 0 || page >= p.num_pages) {   // reads as zeros
-                    S.err = NSA_ERR_BAD_INDEX;
-                    page = p.num_pages;
-                }
+            if (nx_live && (nx_page < 0 || nx_page >= p.num_pages)) {   // reads as zeros
+                S.err = NSA_ERR_BAD_INDEX;
+                nx_page = p.num_pages;
             }
-            const unsigned mask = __ballot_sync(0xffffffffu, live);
-            const int g = k.g;
+            const unsigned mask = __ballot_sync(0xffffffffu, nx_live);
 #pragma unroll
             for (int i = 0; i < kRun; ++i)
                 if (i == pending) {
-                    page_q[i] = page;
-                    row_q[i] = row;
-                    g_q[i] = g;
+                    page_q[i] = nx_page;
+                    row_q[i] = nx_row;
+                    g_q[i] = nx_g;
                     mask_q[i] = mask;
                 }
-            if (!(ok = load(kmap, Stages::k(tk), page, row, g, mask))) break;
+            if (!(ok = load(kmap, Stages::k(tk), nx_page, nx_row, nx_g, mask))) break;
             ++tk;
             ++pending;
-            ++j;
+            if (!(ok = advance())) break;
             if (pending < kRun) continue;
         }
         if (pending == 0) break;
@@ -583,8 +618,9 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
     __syncwarp();
 }
 
-// paged_few.cu: units of at most `rows` = 16 or 32 query rows.
-cudaError_t launch_paged_few(const Params& P, int f16, int rows, int grid, const CUtensorMap& q,
-                             const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream);
+// paged_few.cu: units of at most kFewRows query rows.
+constexpr int kFewRows = 16;
+cudaError_t launch_paged_few(const Params& P, int f16, int grid, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, cudaStream_t stream);
 
 }  // namespace nsa

@@ -4,7 +4,7 @@
 // With a tile of 128 query rows per unit (paged_attn.cu) a single token's G rows lie in one
 // warp's TMEM lanes: that warp alone works through 128 keys a row, and the tensor pipe
 // multiplies rows that do not exist.  Here keys and value columns are the 128 rows of the
-// products and the N query rows (16 or 32) their columns:
+// products and the N = 16 query rows their columns:
 //     S^T [128 keys x N] = K Q^T          O^T [D columns x N] += V^T P^T
 // so a thread holds one key's scores of all N rows, the softmax of a tile is N values a
 // thread on all four schedulers, and a product is N / 128 of the work.  P^T goes through
@@ -29,16 +29,16 @@
 namespace nsa {
 namespace {
 
+constexpr int N = 16;
 constexpr int kFewThreads = 384;
 constexpr int kFewSoftmax = 8;
 
-template <int D, int N>
+template <int D>
 struct alignas(1024) FewSmem {
     static constexpr int kHalves = D / 64;
     // 32 KB (D = 128) or 16 KB (D = 64) each; what fits next to Q and P^T
-    static constexpr int kStages = (N == 16 ? 6 : 4) * (D == 128 ? 1 : 2);
-    // S^T tiles of a stream ahead of its P V: as many as its stages allow, two at most
-    static constexpr int kAhead = kStages >= 6 ? 2 : 1;
+    static constexpr int kStages = D == 128 ? 6 : 12;
+    static constexpr int kAhead = 2;          // S^T tiles of a stream ahead of its P V
     uint8_t q[2][kHalves][N * 128];           // [unit parity][64 columns][row]
     uint8_t pt[2][2][2][N * 128];             // [stream][buffer][64 keys][row]
     uint8_t kv[kStages][kHalves][kRegion];
@@ -70,10 +70,9 @@ __device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, float* v) {
         : "r"(taddr) : "memory");
 }
 
-// Reduces v[0 .. N) over the 32 lanes at N - 1 (+ 1 for N = 16) shuffles: at each step a lane
-// keeps half of its values.  Lane i ends with the result of value i (N = 16: lanes i and
-// i + 16).
-template <int N, class Op>
+// Reduces v[0 .. 16) over the 32 lanes at 16 shuffles: at each of the first steps a lane keeps
+// half of its values.  Lanes i and i + 16 end with the result of value i.
+template <class Op>
 __device__ __forceinline__ float transpose_reduce(float (&v)[N], int lane, Op op) {
 #pragma unroll
     for (int n = N / 2; n >= 1; n >>= 1) {
@@ -84,15 +83,14 @@ __device__ __forceinline__ float transpose_reduce(float (&v)[N], int lane, Op op
             v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, n));
         }
     }
-    if (N == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-template <int F16, int D, int N, bool SEL>
+template <int F16, int D, bool SEL>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_paged_few(const Params P, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using Smem = FewSmem<D, N>;
+    using Smem = FewSmem<D>;
     constexpr int kHalves = Smem::kHalves, kStages = Smem::kStages;
     using Stages = Ring<2, kStages / 2, Smem::kAhead>;
     constexpr uint32_t kCols = 8 * N;             // TMEM: S^T [stream][buffer], O^T [stream][unit parity]
@@ -317,137 +315,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint32_t chunk = (uint32_t)((key & 63) >> 3);
         const uint32_t pt0 = smem_u32(S.pt[st][0][key >> 6]) + (uint32_t)(key & 7) * 2u;
         int items = 0, tiles = 0, units = 0, meets = 0;
-        int o_cnt[2] = {0, 0};
+        int o_next[2] = {0, 0};           // sums each stream has begun
         bool ok = true;
         auto meet = [&]() -> bool {           // the four warps of the stream
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.meet[st]);
             return wait(&S.meet[st], meets++ & 1);
         };
-        for (int at = 0;; ++at) {
-            if (!(ok = fetch_piece(S, wait, at))) break;
-            const Piece& k = S.ring[at % kRing];
-            if (!k.more) break;
-            const int* list = S.list[at % kRing];
-            const int rows = k.ntok * p.G, p0 = k.p0, p1 = k.p1, nt = p1 - p0;
-            const int n0 = (nt + 1 - (tiles & 1)) >> 1, n1 = nt - n0;
-            const int from = p0 + ((tiles & 1) ^ st);
-            tiles += nt;
-            float m[N], l[N];
-#pragma unroll
-            for (int r = 0; r < N; ++r) {
-                m[r] = -CUDART_INF_F;
-                l[r] = 0.f;
-            }
-            for (int j = from; j < p1; j += 2, ++items) {
-                // rows [r0, r1) see this thread's key
-                int r0 = 0, r1 = rows;
-                if (SEL) {
-                    int l0, h0, l1, h1;
-                    tile_cols<SEL>(P, k, list, j, l0, h0, l1, h1);
-                    if (key < 64 ? (key < l0 || key > h0) : (key < l1 || key > h1)) r1 = 0;
-                } else {
-                    // token t (position pos0 + t) sees key x iff pos0 + t - W < x <= pos0 + t
-                    const int ahead = (k.tile0 + j) * kTileKeys + key - k.pos0;
-                    r0 = ahead > 0 ? (ahead < k.ntok ? ahead * p.G : N) : 0;
-                    if (p.swin > 0) {
-                        const int t1 = ahead + p.swin;           // tokens below t1
-                        r1 = t1 <= 0 ? 0 : (t1 < k.ntok ? t1 * p.G : rows);
-                    }
-                }
-                if (!(ok = wait(&S.s_full[st][items & 1], (items >> 1) & 1))) break;
-                tc_fence_after();
-                float s[N];
-#pragma unroll
-                for (int x = 0; x < N; x += 16) tmem_ld16_sync(tS + (uint32_t)((items & 1) * N + x), s + x);
-                bool grow = false;
-#pragma unroll
-                for (int r = 0; r < N; ++r) {
-                    s[r] = r >= r0 && r < r1 ? s[r] * c : -CUDART_INF_F;
-                    grow |= s[r] > m[r] + kLazy;
-                }
-                grow = __any_sync(0xffffffffu, grow);
-                if (lane == 0) S.flag[items & 1][st][quad] = grow;
-                if (!(ok = meet())) break;
-                const int4 f = *reinterpret_cast<const int4*>(S.flag[items & 1][st]);
-                if (f.x | f.y | f.z | f.w) {
-                    // the tile's maximum of every row, over lanes and warps
-                    float t[N];
-#pragma unroll
-                    for (int r = 0; r < N; ++r) t[r] = s[r];
-                    const float top = transpose_reduce<N>(t, lane, [](float a, float b) { return fmaxf(a, b); });
-                    if (lane < N) S.wmax[st][quad][lane] = top;
-                    if (!(ok = meet())) break;
-                    // (O^T: the stream's last P V has to be complete)
-                    if (j != from && !(ok = wait(&S.pv_done[st], (items - 1) & 1))) break;
-                    tc_fence_after();
-                    const uint32_t o0 = tO + (uint32_t)((st * 2 + (o_cnt[st] & 1)) * N);
-#pragma unroll
-                    for (int x = 0; x < N; x += 16) {
-                        float a[16], o[16];
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const int r = x + y;
-                            const float mx = fmaxf(fmaxf(S.wmax[st][0][r], S.wmax[st][1][r]),
-                                                   fmaxf(S.wmax[st][2][r], S.wmax[st][3][r]));
-                            const bool g = mx > m[r] + kLazy;
-                            a[y] = g ? ex2_approx(m[r] - mx) : 1.f;     // m = -inf: 0
-                            if (g) m[r] = mx;
-                            l[r] *= a[y];
-                        }
-                        if (j != from) {
-                            tmem_ld16_sync(o0 + x, o);
-#pragma unroll
-                            for (int y = 0; y < 16; ++y) o[y] *= a[y];
-                            tmem_st16_sync(o0 + x, o);
-                        }
-                    }
-                }
-                const uint32_t pt = pt0 + (uint32_t)(items & 1) * (2 * N * 128);
-#pragma unroll
-                for (int r = 0; r < N; r += 2) {
-                    const float e0 = ex2_approx(s[r] - (m[r] == -CUDART_INF_F ? 0.f : m[r]));
-                    const float e1 = ex2_approx(s[r + 1] - (m[r + 1] == -CUDART_INF_F ? 0.f : m[r + 1]));
-                    l[r] += e0;
-                    l[r + 1] += e1;
-                    const uint32_t w = pack2<F16>(e0, e1);
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(
-                                     pt + (r >> 3) * 1024u + (r & 7) * 128u + ((chunk ^ (r & 7)) << 4)),
-                                 "h"((uint16_t)w) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(
-                                     pt + ((r + 1) >> 3) * 1024u + ((r + 1) & 7) * 128u + ((chunk ^ ((r + 1) & 7)) << 4)),
-                                 "h"((uint16_t)(w >> 16)) : "memory");
-                }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_full[st][items & 1]);
-            }
-            if (!ok) break;
-            const int par = units & 1;
+        // A finished unit's output.  It waits for the unit's last P V and for the other stream,
+        // so it is left until the first tile of the next unit is on its way.
+        struct Done { int at, par, phase, nt, n0, n1, c0, c1; };
+        Done done{-1, 0, 0, 0, 0, 0, 0, 0};
+        auto finish = [&]() -> bool {
+            const Piece& k = S.ring[done.at % kRing];
+            const int par = done.par, nt = done.nt, rows = k.ntok * p.G;
             if (nt > 0) {
-                // the rows' references and sums, for both streams' threads
-                if (quad == 0 && lane == 0) {
-#pragma unroll
-                    for (int r = 0; r < N; ++r) S.m[par][st][r] = m[r];
-                }
-                const float lsum = transpose_reduce<N>(l, lane, [](float a, float b) { return a + b; });
-                if (lane < N) S.l[par][st][quad][lane] = lsum;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.xbar);
-                ok = wait(&S.xbar, units & 1);
-                if (ok && n0 > 0) ok = wait(&S.o_full[0][o_cnt[0] & 1], (o_cnt[0] >> 1) & 1);
-                if (ok && n1 > 0) ok = wait(&S.o_full[1][o_cnt[1] & 1], (o_cnt[1] >> 1) & 1);
-                if (!ok) break;
+                bool fine = wait(&S.xbar, done.phase);
+                if (fine && done.n0 > 0) fine = wait(&S.o_full[0][done.c0 & 1], (done.c0 >> 1) & 1);
+                if (fine && done.n1 > 0) fine = wait(&S.o_full[1][done.c1 & 1], (done.c1 >> 1) & 1);
+                if (!fine) return false;
                 tc_fence_after();
             }
             // this thread: value column `key` of half of the rows (the other half: the other
             // warpgroup)
             const int slot = k.slot, tok0 = k.tok0, hq0 = k.g * p.G;
-            const uint32_t o0 = tO + (uint32_t)((o_cnt[0] & 1) * N), o1 = tO + (uint32_t)((2 + (o_cnt[1] & 1)) * N);
-#pragma unroll 1
-            for (int x = st * (N / 2); x < (st + 1) * (N / 2); x += 8) {
-                if (x >= rows) break;
+            const uint32_t o0 = tO + (uint32_t)((done.c0 & 1) * N), o1 = tO + (uint32_t)((2 + (done.c1 & 1)) * N);
+            const int x = st * (N / 2);
+            if (x < rows) {
                 float a[8], b[8];
                 tmem_ld8_sync(o0 + x, a);
                 tmem_ld8_sync(o1 + x, b);
@@ -484,15 +378,128 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (n0 > 0) mbar_arrive(&S.o_empty[0][o_cnt[0] & 1]);
-                    if (n1 > 0) mbar_arrive(&S.o_empty[1][o_cnt[1] & 1]);
+                    if (done.n0 > 0) mbar_arrive(&S.o_empty[0][done.c0 & 1]);
+                    if (done.n1 > 0) mbar_arrive(&S.o_empty[1][done.c1 & 1]);
                 }
-                o_cnt[0] += n0 > 0;
-                o_cnt[1] += n1 > 0;
+            }
+            release_piece(S, lane, done.at);
+            done.at = -1;
+            return true;
+        };
+        for (int at = 0;; ++at) {
+            if (!(ok = fetch_piece(S, wait, at))) break;
+            const Piece& k = S.ring[at % kRing];
+            if (!k.more) break;
+            const int* list = S.list[at % kRing];
+            const int rows = k.ntok * p.G, p0 = k.p0, p1 = k.p1, nt = p1 - p0;
+            const int n0 = (nt + 1 - (tiles & 1)) >> 1, n1 = nt - n0;
+            const int from = p0 + ((tiles & 1) ^ st);
+            tiles += nt;
+            float m[N], l[N];
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                m[r] = -CUDART_INF_F;
+                l[r] = 0.f;
+            }
+            for (int j = from; j < p1; j += 2, ++items) {
+                // rows [r0, r1) see this thread's key
+                int r0 = 0, r1 = rows;
+                if (SEL) {
+                    int l0, h0, l1, h1;
+                    tile_cols<SEL>(P, k, list, j, l0, h0, l1, h1);
+                    if (key < 64 ? (key < l0 || key > h0) : (key < l1 || key > h1)) r1 = 0;
+                } else {
+                    // token t (position pos0 + t) sees key x iff pos0 + t - W < x <= pos0 + t
+                    const int ahead = (k.tile0 + j) * kTileKeys + key - k.pos0;
+                    r0 = ahead > 0 ? (ahead < k.ntok ? ahead * p.G : N) : 0;
+                    if (p.swin > 0) {
+                        const int t1 = ahead + p.swin;           // tokens below t1
+                        r1 = t1 <= 0 ? 0 : (t1 < k.ntok ? t1 * p.G : rows);
+                    }
+                }
+                if (!(ok = wait(&S.s_full[st][items & 1], (items >> 1) & 1))) break;
+                tc_fence_after();
+                float s[N];
+                tmem_ld16_sync(tS + (uint32_t)((items & 1) * N), s);
+                bool grow = false;
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    s[r] = r >= r0 && r < r1 ? s[r] * c : -CUDART_INF_F;
+                    grow |= s[r] > m[r] + kLazy;
+                }
+                grow = __any_sync(0xffffffffu, grow);
+                if (lane == 0) S.flag[items & 1][st][quad] = grow;
+                if (!(ok = meet())) break;
+                const int4 f = *reinterpret_cast<const int4*>(S.flag[items & 1][st]);
+                if (f.x | f.y | f.z | f.w) {
+                    // the tile's maximum of every row, over lanes and warps
+                    float t[N];
+#pragma unroll
+                    for (int r = 0; r < N; ++r) t[r] = s[r];
+                    const float top = transpose_reduce(t, lane, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < N) S.wmax[st][quad][lane] = top;
+                    if (!(ok = meet())) break;
+                    // (O^T: the stream's last P V has to be complete)
+                    if (j != from && !(ok = wait(&S.pv_done[st], (items - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t o0 = tO + (uint32_t)((st * 2 + (o_next[st] & 1)) * N);
+                    float a[N], o[N];
+#pragma unroll
+                    for (int r = 0; r < N; ++r) {
+                        const float mx = fmaxf(fmaxf(S.wmax[st][0][r], S.wmax[st][1][r]),
+                                               fmaxf(S.wmax[st][2][r], S.wmax[st][3][r]));
+                        const bool g = mx > m[r] + kLazy;
+                        a[r] = g ? ex2_approx(m[r] - mx) : 1.f;     // m = -inf: 0
+                        if (g) m[r] = mx;
+                        l[r] *= a[r];
+                    }
+                    if (j != from) {
+                        tmem_ld16_sync(o0, o);
+#pragma unroll
+                        for (int r = 0; r < N; ++r) o[r] *= a[r];
+                        tmem_st16_sync(o0, o);
+                    }
+                }
+                const uint32_t pt = pt0 + (uint32_t)(items & 1) * (2 * N * 128);
+#pragma unroll
+                for (int r = 0; r < N; r += 2) {
+                    const float e0 = ex2_approx(s[r] - (m[r] == -CUDART_INF_F ? 0.f : m[r]));
+                    const float e1 = ex2_approx(s[r + 1] - (m[r + 1] == -CUDART_INF_F ? 0.f : m[r + 1]));
+                    l[r] += e0;
+                    l[r + 1] += e1;
+                    const uint32_t w = pack2<F16>(e0, e1);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                                     pt + (r >> 3) * 1024u + (r & 7) * 128u + ((chunk ^ (r & 7)) << 4)),
+                                 "h"((uint16_t)w) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                                     pt + ((r + 1) >> 3) * 1024u + ((r + 1) & 7) * 128u + ((chunk ^ ((r + 1) & 7)) << 4)),
+                                 "h"((uint16_t)(w >> 16)) : "memory");
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_full[st][items & 1]);
+                if (done.at >= 0 && !(ok = finish())) break;
+            }
+            if (!ok) break;
+            if (done.at >= 0 && !(ok = finish())) break;     // (no tile of this unit for the stream)
+            done = {at, units & 1, units & 1, nt, n0, n1, o_next[0], o_next[1]};
+            if (nt > 0) {
+                // the rows' references and sums, for both streams' threads
+                if (quad == 0 && lane == 0) {
+#pragma unroll
+                    for (int r = 0; r < N; ++r) S.m[done.par][st][r] = m[r];
+                }
+                const float lsum = transpose_reduce(l, lane, [](float a, float b) { return a + b; });
+                if (lane < N) S.l[done.par][st][quad][lane] = lsum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.xbar);
+                o_next[0] += n0 > 0;
+                o_next[1] += n1 > 0;
                 ++units;
             }
-            release_piece(S, lane, at);
         }
+        if (ok && done.at >= 0) finish();
     }
 
     // ---- teardown: every role has left its loop (all waits are bounded) and the issuers
@@ -504,34 +511,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (tid == 0) finish_status(p.st, S.err, cta, grid);
 }
 
-template <int F16, int D, int N, bool SEL>
+template <int F16, int D, bool SEL>
 cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUtensorMap& kmap,
                    const CUtensorMap& vmap, cudaStream_t stream) {
-    const size_t smem = sizeof(FewSmem<D, N>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_paged_few<F16, D, N, SEL>,
+    const size_t smem = sizeof(FewSmem<D>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_paged_few<F16, D, SEL>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_paged_few<F16, D, N, SEL><<<grid, kFewThreads, smem, stream>>>(P, qmap, kmap, vmap);
+    k_paged_few<F16, D, SEL><<<grid, kFewThreads, smem, stream>>>(P, qmap, kmap, vmap);
     return cudaGetLastError();
 }
 
 template <int F16, int D>
-cudaError_t dispatch(const Params& P, int rows, int grid, const CUtensorMap& q, const CUtensorMap& k,
-                     const CUtensorMap& v, cudaStream_t stream) {
-    if (P.a.bidx)
-        return rows == 16 ? launch<F16, D, 16, true>(P, grid, q, k, v, stream)
-                          : launch<F16, D, 32, true>(P, grid, q, k, v, stream);
-    return rows == 16 ? launch<F16, D, 16, false>(P, grid, q, k, v, stream)
-                      : launch<F16, D, 32, false>(P, grid, q, k, v, stream);
+cudaError_t dispatch(const Params& P, int grid, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                     cudaStream_t stream) {
+    return P.a.bidx ? launch<F16, D, true>(P, grid, q, k, v, stream)
+                    : launch<F16, D, false>(P, grid, q, k, v, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_few(const Params& P, int f16, int rows, int grid, const CUtensorMap& q,
-                             const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+cudaError_t launch_paged_few(const Params& P, int f16, int grid, const CUtensorMap& q, const CUtensorMap& k,
+                             const CUtensorMap& v, cudaStream_t stream) {
     if (P.a.d == 64)
-        return f16 ? dispatch<1, 64>(P, rows, grid, q, k, v, stream) : dispatch<0, 64>(P, rows, grid, q, k, v, stream);
-    return f16 ? dispatch<1, 128>(P, rows, grid, q, k, v, stream) : dispatch<0, 128>(P, rows, grid, q, k, v, stream);
+        return f16 ? dispatch<1, 64>(P, grid, q, k, v, stream) : dispatch<0, 64>(P, grid, q, k, v, stream);
+    return f16 ? dispatch<1, 128>(P, grid, q, k, v, stream) : dispatch<0, 128>(P, grid, q, k, v, stream);
 }
 
 }  // namespace nsa
