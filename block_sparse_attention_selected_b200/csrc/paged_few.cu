@@ -29,7 +29,7 @@
 namespace nsa {
 namespace {
 
-constexpr int N = 16;
+constexpr int N = kFewRows;
 constexpr int kFewThreads = 384;
 constexpr int kFewSoftmax = 8;
 

@@ -22,16 +22,18 @@ import ctypes
 
 import torch
 
-from . import NSA_F16, NsaError, _check, _need, _ws_cache, get_workspace, load_library
+from . import NSA_F16, NsaError, _check, _ws_cache, get_workspace, load_library
 
 __all__ = ["nsa_sel_paged_plan", "nsa_sel_paged_write_kv", "nsa_sel_paged_attn_workspace_size",
            "nsa_sel_paged_attn_fwd", "nsa_sel_paged_sel_fwd"]
 
 # A decode step makes these calls once per layer on kernels of a few microseconds, so the
-# host path is kept short: plain comparisons, and the stream and device queries that
-# torch's own generated code uses.
+# host path is kept short: each tensor is tested by one expression, and looked at again only
+# to say what is wrong with it; the stream and device queries are those that torch's own
+# generated code uses.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 _ELEM = {torch.bfloat16: 0, torch.float16: NSA_F16}
 
 
@@ -42,64 +44,83 @@ class _Cache(ctypes.Structure):   # nsa_paged_cache_t
                 ("head_dim", ctypes.c_int)]
 
 
-def _call(fn: str, dev: torch.device, *args):
+def _call(fn: str, index: int, *args):
     """Calls the library with the tensors' device current."""
     f = getattr(load_library(), fn)
-    if dev.index == _current_device():
+    if index == _current_device():
         code = f(*args)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             code = f(*args)
     if code:
         _check(fn, code)
 
 
-def _need_strided(t, name, dtype, ndim, dev):
-    """A CUDA tensor whose last dimension is adjacent; other strides are free."""
+def _refuse(t, name, dtype, ndim, index):
+    """Raises for a tensor that failed its test; returns where the test was too strict."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError(f"{name} must have adjacent columns (stride 1 in its last dimension)")
 
 
-def _strides(t):
-    # an empty tensor may have any strides; nothing is read through them
-    return t.stride()[:2] if t.numel() else (0, 0)
+def _packed(t, name, dtype, ndim, index):
+    """A contiguous CUDA tensor's pointer."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == ndim
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, ndim, index)
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _cache_arg(k_cache, v_cache, et, dev):
-    _need_strided(k_cache, "k_cache", et, 4, dev)
-    _need_strided(v_cache, "v_cache", et, 4, dev)
-    shape, strides = k_cache.shape, k_cache.stride()
+def _strided(t, name, dtype, ndim, index):
+    """The strides of a CUDA tensor whose last dimension is adjacent; the others are free."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == ndim):
+        _refuse(t, name, dtype, ndim, index)
+    strides = t.stride()
+    if strides[-1] != 1:
+        if not t.numel():       # nothing is read through an empty tensor's strides
+            return (0,) * ndim
+        if t.shape[-1] > 1:
+            raise ValueError(f"{name} must have adjacent columns (stride 1 in its last dimension)")
+    return strides
+
+
+def _cache_arg(k_cache, v_cache, et, index):
+    strides = _strided(k_cache, "k_cache", et, 4, index)
+    other = _strided(v_cache, "v_cache", et, 4, index)
+    shape = k_cache.shape
     if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if strides != v_cache.stride():
+    if strides != other:
         raise ValueError("k_cache and v_cache must have the same strides")
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides[:3], *shape)
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides[:3], *shape), shape
 
 
 def _elem(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     et = t.dtype
     if et not in _ELEM:
         raise TypeError(f"{name}: expected bfloat16 or float16, got {et}")
-    return et, _ELEM[et]
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return et, _ELEM[et], t.get_device()
 
 
-def _table_arg(block_table, R, dev):
+def _table_arg(block_table, R, index):
     """(pointer, width, row stride) of a block table of R rows."""
-    _need_strided(block_table, "block_table", torch.int32, 2, dev)
+    strides = _strided(block_table, "block_table", torch.int32, 2, index)
     rows, width = block_table.shape
     if rows != R:
         raise ValueError("block_table needs one row per request")
-    return block_table.data_ptr(), width, max(block_table.stride(0), width) if R == 1 else block_table.stride(0)
+    return block_table.data_ptr(), width, max(strides[0], width) if R == 1 else strides[0]
 
 
 def nsa_sel_paged_plan(new_lens, cached_lens, free_pages, block_table, page_size, total_tokens):
@@ -113,22 +134,23 @@ def nsa_sel_paged_plan(new_lens, cached_lens, free_pages, block_table, page_size
     total_tokens: host int, at least the sum of new_lens; rows behind it get slot -1.
     pages_used[0] is what the step needs of free_pages; missing pages are -1 in the table,
     and slots on them -1."""
-    dev = new_lens.device
-    _need(new_lens, "new_lens", torch.int32, 1, dev)
-    _need(cached_lens, "cached_lens", torch.int32, 1, dev)
-    _need(free_pages, "free_pages", torch.int32, 1, dev)
+    if not isinstance(new_lens, torch.Tensor) or not new_lens.is_cuda:
+        raise ValueError("new_lens must be a CUDA tensor")
+    index, int32 = new_lens.get_device(), torch.int32
+    new = _packed(new_lens, "new_lens", int32, 1, index)
+    cached = _packed(cached_lens, "cached_lens", int32, 1, index)
+    free = _packed(free_pages, "free_pages", int32, 1, index)
     R, T = new_lens.shape[0], int(total_tokens)
     if cached_lens.shape[0] != R:
         raise ValueError("new_lens and cached_lens must have the same length")
-    table = _table_arg(block_table, R, dev)
+    table = _table_arg(block_table, R, index)
     if T < 0:
         raise ValueError("total_tokens must not be negative")
     cu, kv_lens, used = new_lens.new_empty(R + 1), new_lens.new_empty(R), new_lens.new_empty(1)
     slots, positions = new_lens.new_empty(T, dtype=torch.int64), new_lens.new_empty(T)
-    _call("nsa_sel_paged_plan", dev, new_lens.data_ptr(), cached_lens.data_ptr(), R,
-          free_pages.data_ptr(), free_pages.shape[0], *table, int(page_size), T, cu.data_ptr(),
-          kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), used.data_ptr(),
-          _raw_stream(dev.index))
+    _call("nsa_sel_paged_plan", index, new, cached, R, free, free_pages.shape[0], *table, int(page_size), T,
+          cu.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), used.data_ptr(),
+          _raw_stream(index))
     return cu, kv_lens, slots, positions, used
 
 
@@ -137,17 +159,16 @@ def nsa_sel_paged_write_kv(k, v, slots, k_cache, v_cache):
 
     k and v may be slices of a wider tensor (a fused QKV projection) whose strides are
     multiples of 8 elements."""
-    dev = k.device
-    et, _ = _elem(k, "k")
-    _need_strided(k, "k", et, 3, dev)
-    _need_strided(v, "v", et, 3, dev)
-    _need(slots, "slots", torch.int64, 1, dev)
-    cache = _cache_arg(k_cache, v_cache, et, dev)
-    shape = k.shape
-    if v.shape != shape or shape[0] != slots.shape[0] or shape[1] != cache.hkv or shape[2] != cache.head_dim:
+    et, _, index = _elem(k, "k")
+    ks = _strided(k, "k", et, 3, index)
+    vs = _strided(v, "v", et, 3, index)
+    at = _packed(slots, "slots", torch.int64, 1, index)
+    cache, cshape = _cache_arg(k_cache, v_cache, et, index)
+    T, hkv, d = shape = k.shape
+    if v.shape != shape or T != slots.shape[0] or hkv != cshape[2] or d != cshape[3]:
         raise ValueError("inconsistent shapes")
-    _call("nsa_sel_paged_write_kv", dev, k.data_ptr(), v.data_ptr(), *_strides(k), *_strides(v),
-          slots.data_ptr(), shape[0], ctypes.byref(cache), _raw_stream(dev.index))
+    _call("nsa_sel_paged_write_kv", index, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], at, T,
+          ctypes.byref(cache), _raw_stream(index))
 
 
 def nsa_sel_paged_attn_workspace_size(total_tokens, num_seqs, hq, hkv, head_dim) -> int:
@@ -160,52 +181,51 @@ def nsa_sel_paged_attn_workspace_size(total_tokens, num_seqs, hq, hkv, head_dim)
 _workspace_bytes: dict = {}   # head_dim -> bytes: the size depends on nothing else
 
 
-def _paged_workspace(T, R, hq, hkv, d, dev, stream):
+def _paged_workspace(T, R, hq, hkv, d, q, stream):
     nbytes = _workspace_bytes.get(d)
     if nbytes is None:
         nbytes = _workspace_bytes[d] = nsa_sel_paged_attn_workspace_size(T, R, hq, hkv, d)
     # A call that is being captured takes its workspace from the graph's own memory: the
     # cached one would be shared with other graphs and with eager calls, which may overlap
     # with a replay.
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    ws = _ws_cache.get((dev, stream))
-    return ws if ws is not None and ws.numel() >= nbytes else get_workspace(nbytes, dev)
+    if _capturing():
+        return q.new_empty(nbytes, dtype=torch.uint8)
+    ws = _ws_cache.get((q.device, stream))
+    return ws if ws is not None and ws.numel() >= nbytes else get_workspace(nbytes, q.device)
 
 
 def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection, scale, window_size,
             out, lse, with_lse, workspace):
-    dev = q.device
-    et, flag = _elem(q, "q")
-    _need_strided(q, "q", et, 3, dev)
-    cache = _cache_arg(k_cache, v_cache, et, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
-    _need(kv_lens, "kv_lens", torch.int32, 1, dev)
+    et, flag, index = _elem(q, "q")
+    qs = _strided(q, "q", et, 3, index)
+    cache, cshape = _cache_arg(k_cache, v_cache, et, index)
+    cu = _packed(cu_seqlens, "cu_seqlens", torch.int32, 1, index)
+    kv = _packed(kv_lens, "kv_lens", torch.int32, 1, index)
     T, hq, d = shape = q.shape
     R = kv_lens.shape[0]
-    table = _table_arg(block_table, R, dev)
-    if d != cache.head_dim or cu_seqlens.shape[0] != R + 1:
+    table = _table_arg(block_table, R, index)
+    if d != cshape[3] or cu_seqlens.shape[0] != R + 1:
         raise ValueError("inconsistent shapes")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = q.new_empty(shape)
+        to = out.data_ptr()
     else:
-        _need(out, "out", et, 3, dev)
+        to = _packed(out, "out", et, 3, index)
         if out.shape != shape:
             raise ValueError("out must have the shape of q")
+    lse_to = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, 2, dev)
+        lse_to = _packed(lse, "lse", torch.float32, 2, index)
         if lse.shape != (hq, T):
             raise ValueError("lse must be [hq, T]")
     elif with_lse:
         lse = q.new_empty((hq, T), dtype=torch.float32)
-    stream = _raw_stream(dev.index)
-    ws = workspace
-    if ws is None:
-        ws = _paged_workspace(T, R, hq, cache.hkv, d, dev, stream)
-    _call(fn, dev, q.data_ptr(), *_strides(q), T, hq, ctypes.byref(cache), cu_seqlens.data_ptr(),
-          kv_lens.data_ptr(), R, *table, *selection, float(d ** -0.5 if scale is None else scale),
-          int(window_size), out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
-          ws.numel(), stream, flag)
+        lse_to = lse.data_ptr()
+    stream = _raw_stream(index)
+    ws = workspace if workspace is not None else _paged_workspace(T, R, hq, cshape[2], d, q, stream)
+    _call(fn, index, q.data_ptr(), qs[0], qs[1], T, hq, ctypes.byref(cache), cu, kv, R, *table, *selection,
+          d ** -0.5 if scale is None else float(scale), int(window_size), to, lse_to, ws.data_ptr(), ws.numel(),
+          stream, flag)
     return out, lse
 
 
@@ -229,9 +249,10 @@ def nsa_sel_paged_sel_fwd(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
     """Selected-block attention over the paged cache: as nsa_sel_paged_attn_fwd, over the
     keys of the blocks block_idx[t, g, :] (int32 [T, hkv, topk], block numbers local to the
     request's sequence, distinct within a row, -1 pads)."""
-    _need(block_idx, "block_idx", torch.int32, 3, q.device)
-    if block_idx.shape[0] != q.shape[0] or block_idx.shape[1] != k_cache.shape[2]:
+    idx = _packed(block_idx, "block_idx", torch.int32, 3, _elem(q, "q")[2])
+    rows, heads, topk = block_idx.shape
+    if rows != q.shape[0] or heads != k_cache.shape[2]:
         raise ValueError("inconsistent shapes")
     return _attend("nsa_sel_paged_sel_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
-                   (block_idx.data_ptr(), block_idx.shape[2], int(block_size)), scale, window_size,
+                   (idx, topk, int(block_size)), scale, window_size,
                    out, lse, with_lse, workspace)

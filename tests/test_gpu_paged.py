@@ -129,9 +129,9 @@ def test_attend_one_long_request_is_split():
 def test_attend_many_tiles_per_block(q_len, group, d):
     # long runs of key tiles and several units on every SM: the rings of stages, the buffers
     # and their barriers go round many times
-    hkv, R = 8, 24
+    hkv, R = 2, 70
     rng = np.random.default_rng(q_len + group)
-    kv = rng.integers(2500, 6000, R)
+    kv = rng.integers(2000, 5000, R)
     kv[:5] = [300, 129, 128, 127, 11]
     run(make_case([q_len] * R, kv.tolist(), group * hkv, hkv, d, 64, seed=30 + group, poison=False))
 
