@@ -571,6 +571,73 @@ def run_next_path(args):
     return line
 
 
+# ------------------------------------------------------------- the paged K/V cache
+
+def run_paged_path(args):
+    """One GPU, CUDA events: one serving step over a paged cache on the workload's shapes.
+    Every sequence is a request whose last --new-tokens tokens are new: plan, write, causal
+    attention over the whole cache, and selected-block attention (the workload's block
+    indices); one JSON line."""
+    import torch
+    import block_sparse_attention_selected_b200 as nsa
+    from block_sparse_attention_selected_b200 import build as nsa_build
+    nsa_build.build()
+    dev, d, page = torch.device("cuda", 0), 128, 64
+    spec = dict(ni.WORKLOADS[args.workload])
+    p = ni.make_problem(name=args.workload, head_dim=d, with_dout=False, **spec)
+    lens = np.diff(p.cu_seqlens.astype(np.int64))
+    new = np.minimum(lens, args.new_tokens)
+    rows = torch.from_numpy(np.concatenate([np.arange(e - n, e) for e, n in zip(p.cu_seqlens[1:], new)])).to(dev)
+    bf = lambda a: torch.from_numpy(a).to(dev).to(torch.bfloat16)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, np.int32)).to(dev)
+    q, k, v, idx = bf(p.q)[rows], bf(p.k), bf(p.v), torch.from_numpy(p.block_idx).to(dev)[rows]
+    pages = int((-(-lens // page)).sum())
+    width = int((-(-lens // page)).max())
+    caches = [torch.zeros(pages, page, p.hkv, d, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    free = torch.randperm(pages, device=dev).to(torch.int32)
+    table = torch.full((p.nseq, width), -1, dtype=torch.int32, device=dev)
+    # the prompts up to the new tokens
+    _, _, slots, _, used = nsa.nsa_sel_paged_plan(i32(lens - new), i32(0 * lens), free, table, page, int((lens - new).sum()))
+    held = torch.ones(p.T, dtype=torch.bool, device=dev)
+    held[rows] = False
+    nsa.nsa_sel_paged_write_kv(k[held], v[held], slots, *caches)
+    free = free[int(used):].contiguous()
+    kn, vn, n_new, n_old, T = k[rows], v[rows], i32(new), i32(lens - new), int(new.sum())
+    names = ("plan_ms", "write_ms", "attend_ms", "select_ms")
+    evs = [torch.cuda.Event(enable_timing=True) for _ in range(5)]
+
+    def step():
+        evs[0].record()
+        cu, kv, slots, _, _ = nsa.nsa_sel_paged_plan(n_new, n_old, free, table, page, T)
+        evs[1].record()
+        nsa.nsa_sel_paged_write_kv(kn, vn, slots, *caches)
+        evs[2].record()
+        nsa.nsa_sel_paged_attn_fwd(q, *caches, cu, kv, table, p.scale)
+        evs[3].record()
+        nsa.nsa_sel_paged_sel_fwd(q, *caches, cu, kv, table, idx, p.block_size, p.scale)
+        evs[4].record()
+    for _ in range(max(args.warmup, 3)):
+        step()
+    torch.cuda.synchronize()
+    times = []
+    for _ in range(args.steps):
+        step()
+        torch.cuda.synchronize()
+        times.append([evs[a].elapsed_time(evs[a + 1]) for a in range(4)])
+    t = np.median(np.asarray(times), axis=0)
+    keys = sum(float((np.arange(L - n, L) + 1).sum()) for L, n in zip(lens, new))
+    line = {"metric": "paged step ms", "path": "paged", "value": round(float(t.sum()), 4), "unit": "ms",
+            "higher_is_better": False, "steps": args.steps, "warmup": max(args.warmup, 3),
+            "status": int(nsa.nsa_sel_check_status()),
+            "config": {"workload": args.workload, "requests": p.nseq, "new_tokens": T, "hq": p.hq, "hkv": p.hkv,
+                       "page_size": page, "block_size": p.block_size, "topk": p.topk},
+            "phases_ms": {n: round(float(x), 4) for n, x in zip(names, t)},
+            "attend_tflops": round(4.0 * d * p.hq * keys / (float(t[2]) * 1e-3) / 1e12, 2),
+            "attend_cache_gbs": round(float(lens.sum()) * p.hkv * d * 4 / (float(t[2]) * 1e-3) / 1e9, 1)}
+    print(json.dumps(line), flush=True)
+    return line
+
+
 # ----------------------------------------------------------------- oracle baselines
 
 def oracle_sample(workload: str, tokens: int, window: int = 0):
@@ -644,9 +711,12 @@ def main(argv=None):
     ap.add_argument("--window", type=int, default=0,
                     help="sliding window of this many keys (0: none); the index becomes the "
                          "sliding branch's: every block the window reaches")
-    ap.add_argument("--path", choices=["attn", "select", "bsfa"], default="attn",
+    ap.add_argument("--path", choices=["attn", "select", "bsfa", "paged"], default="attn",
                     help="attn: the selected attention step (the default line); select: the "
-                         "block-selection step; bsfa: threshold-pruned block attention")
+                         "block-selection step; bsfa: threshold-pruned block attention; paged: "
+                         "one serving step over a paged K/V cache")
+    ap.add_argument("--new-tokens", type=int, default=1,
+                    help="paged: new tokens of every sequence (the last ones)")
     ap.add_argument("--tau", type=float, default=2.0, help="BSFA threshold of every head")
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-cpu-baseline", action="store_true")
@@ -664,7 +734,7 @@ def main(argv=None):
         return 0
     if args.path != "attn":
         if rank == 0:
-            run_next_path(args)
+            (run_paged_path if args.path == "paged" else run_next_path)(args)
         return 0
     dist = None
     if world > 1:

@@ -19,7 +19,7 @@ LIB_CHECKS = os.path.join(HERE, "libnsa_sel_checks.so")
 SOURCES = ["api.cu", "invert.cu", "fwd.cu", "merge.cu", "bwd.cu", "select.cu", "bsfa.cu",
            "paged.cu", "paged_attn.cu", "paged_few.cu",
            "paged_api.cu"]
-HEADERS = ["nsa_common.cuh", "nsa_kernels.h", "paged_attn.cuh"]
+HEADERS = ["nsa_common.cuh", "nsa_kernels.h", "paged.h", "paged_attn.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

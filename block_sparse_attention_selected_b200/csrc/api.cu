@@ -11,6 +11,7 @@
 
 #include "nsa_common.cuh"
 #include "nsa_kernels.h"
+#include "paged.h"
 
 using namespace nsa;
 
@@ -886,7 +887,7 @@ nsa_status_t nsa_sel_check_status(const void* workspace, nsa_stream_t stream_) {
         cudaStreamSynchronize(stream) != cudaSuccess)
         return NSA_ERR_CUDA;
     int code = st.code;
-    for (int i = 0; code == 0 && i < kMaxStatusCtas; ++i) code = st.cta_err[i];
+    for (int i = 0; code == 0 && i < kMaxStatusCtas; ++i) code = cta_status(&st)[i];
     return static_cast<nsa_status_t>(code);
 }
 

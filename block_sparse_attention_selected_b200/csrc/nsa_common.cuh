@@ -22,8 +22,6 @@ constexpr int kTileRows = 128;       // MMA M: (token, head) rows per tile
 constexpr int kMaxTopk = 64;         // entry = token * 64 + slot
 constexpr int kMaxGroup = 128;       // query heads per KV head (a divisor of the 128-row tile)
 
-constexpr int kMaxStatusCtas = 160;  // CTAs with a status byte of their own
-
 // Device status word layout (int32 slots at the start of the workspace).
 struct DevStatus {
     int code;          // first error code recorded (nsa_status_t), 0 = none
@@ -38,11 +36,9 @@ struct DevStatus {
     int pad0;
     unsigned long long index_tag;   // identifies the inputs of the inversion held here
     long long wait_budget;          // cycles a bounded wait may spin (0: kWaitBudgetCycles)
-    unsigned char cta_err[160];     // paged attention: one code per CTA, 0 = none
-    int pad[6];
+    int pad[46];
 };
 static_assert(sizeof(DevStatus) == 256, "status block is 256 bytes");
-static_assert(sizeof(DevStatus::cta_err) == kMaxStatusCtas, "one status byte per CTA");
 
 __device__ __forceinline__ void record_error(DevStatus* st, int code, int where, int a0 = 0,
                                              int a1 = 0) {

@@ -4,18 +4,11 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <stdint.h>
-
-#include "../../include/nsa_sel.h"
 
 namespace nsa {
 
 struct DevStatus;
-
-// Host helpers of the C ABI (api.cu).
-nsa_status_t check_device(int* num_sms, nsa_stream_t stream);
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn();   // null if the driver lacks it
 
 // Everything the index inversion reads and writes.
 struct InvertPlan {
@@ -201,64 +194,6 @@ cudaError_t launch_bsfa_fwd(const int32_t* cu, int nseq, int T, int hq, int hkv,
 cudaError_t launch_select_topk(const float* scores, const int32_t* cu, int nseq, int T, int hkv,
                                int nb_stride, int bs, int topk, int init_blocks, int local_blocks,
                                int32_t* bidx, DevStatus* st, cudaStream_t stream);
-
-// Paged K/V cache (paged.cu, paged_attn.cu, paged_api.cu).
-struct PagedPlanArgs {
-    const int32_t* new_lens; // [R]
-    const int32_t* old_lens; // [R]
-    int R;
-    const int32_t* free_pages;
-    int num_free;
-    int32_t* table;          // [R, width], row stride table_stride
-    int width;
-    long long table_stride;
-    int ps;                  // tokens per page
-    int T;                   // rows of slots and positions
-    int32_t* cu;             // [R + 1]
-    int32_t* kv_lens;        // [R]
-    int64_t* slots;          // [T]
-    int32_t* positions;      // [T]
-    int32_t* pages_used;     // [1]
-};
-cudaError_t launch_paged_plan(const PagedPlanArgs& p, int num_sms, cudaStream_t stream);
-
-// Strides in elements of 16 bits.
-struct PagedWriteArgs {
-    const uint16_t* k;
-    const uint16_t* v;
-    long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;
-    const int64_t* slots;    // [T]
-    int T, hkv, d;
-    uint16_t* k_cache;
-    uint16_t* v_cache;
-    int num_pages, ps;
-    long long page_stride, token_stride, head_stride;
-};
-cudaError_t launch_paged_write(const PagedWriteArgs& p, cudaStream_t stream);
-
-struct PagedAttnArgs {
-    const uint16_t* q;       // [T, hq, d]
-    long long q_token_stride, q_head_stride;
-    const uint16_t* k;       // the caches
-    const uint16_t* v;
-    long long page_stride, token_stride, head_stride;
-    int num_pages, ps;
-    int T, R, hq, hkv, G, d;
-    const int32_t* cu;       // [R + 1] new tokens
-    const int32_t* kv_lens;  // [R] tokens in the cache, the new ones included
-    const int32_t* table;    // [R, table_width]
-    int table_width;
-    long long table_stride;
-    const int32_t* bidx;     // [T, hkv, topk] or null: every visible key
-    int topk, bs;
-    int swin;                // sliding window in keys (0: none)
-    float scale_log2;        // scale * log2(e)
-    uint16_t* out;           // [T, hq, d]
-    float* lse;              // [hq, T] or null
-    DevStatus* st;
-};
-size_t paged_attn_workspace(int d);   // bytes, the status block included
-cudaError_t launch_paged_attn(const PagedAttnArgs& p, int f16, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_validate(const int32_t* cu, int nseq, int T, int hkv, const int32_t* bidx,
                             int topk, int bs, DevStatus* st, cudaStream_t stream);

@@ -7,8 +7,7 @@
 // order, so that their places in it are exclusive prefix sums over the requests.
 #include <algorithm>
 
-#include "nsa_common.cuh"
-#include "nsa_kernels.h"
+#include "paged.h"
 
 namespace nsa {
 namespace {

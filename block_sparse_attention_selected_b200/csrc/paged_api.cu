@@ -1,7 +1,6 @@
 // paged_api.cu -- the C ABI of the paged K/V cache (include/nsa_sel.h): argument checks
 // before any launch, then the launches of paged.cu and paged_attn.cu.
-#include "nsa_common.cuh"
-#include "nsa_kernels.h"
+#include "paged.h"
 
 using namespace nsa;
 

@@ -21,8 +21,7 @@
 
 #include <math_constants.h>
 
-#include "nsa_common.cuh"
-#include "nsa_kernels.h"
+#include "paged.h"
 
 namespace nsa {
 
@@ -430,10 +429,11 @@ struct Waiter {
 
 // One status byte per CTA, always written: nothing has to be cleared before the call.
 __device__ __forceinline__ void finish_status(DevStatus* st, int err, int cta, int grid) {
-    st->cta_err[cta] = (unsigned char)err;
+    cta_status(st)[cta] = (unsigned char)err;
     if (cta == 0) {
         st->code = 0;
-        for (int i = grid; i < kMaxStatusCtas; ++i) st->cta_err[i] = 0;
+        st->index_tag = 0;      // an index inversion left in this workspace is gone
+        for (int i = grid; i < kMaxStatusCtas; ++i) cta_status(st)[i] = 0;
     }
 }
 
