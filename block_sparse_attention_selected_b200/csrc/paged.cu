@@ -105,33 +105,36 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
 constexpr int kWriteThreads = 256;
 constexpr int kWriteUnroll = 4;
 
-// One thread moves kWriteUnroll 16-byte pieces of K and of V, all loads before the first
-// store.  Bound by memory: each row is read once and written once.
-__global__ void __launch_bounds__(kWriteThreads) k_paged_write(PagedWriteArgs p) {
-    const int per_head = p.d / 8, per_tok = p.hkv * per_head;
-    const long long total = (long long)p.T * per_tok;
-    const long long base = (long long)blockIdx.x * (kWriteThreads * kWriteUnroll) + threadIdx.x;
-    uint4 kv[kWriteUnroll][2];
-    long long dst[kWriteUnroll];
+// Blocks take whole tokens (one at least), threads 16-byte pieces of K and of V, a thread's
+// loads before its first store.  Bound by memory: each row is read once and written once.
+// Page and row sizes are powers of two but the number of heads is not: the one division left
+// is of 32-bit numbers.
+__global__ void __launch_bounds__(kWriteThreads) k_paged_write(PagedWriteArgs p, int tokens) {
+    const int per_head_log2 = 28 - __clz(p.d), per_tok = p.hkv << per_head_log2, ps_log2 = 31 - __clz(p.ps);
+    const int t0 = blockIdx.x * tokens, n = min(tokens, p.T - t0) * per_tok;
+    for (int first = threadIdx.x; first < n; first += kWriteThreads * kWriteUnroll) {
+        uint4 kv[kWriteUnroll][2];
+        long long dst[kWriteUnroll];
 #pragma unroll
-    for (int u = 0; u < kWriteUnroll; ++u) {
-        const long long i = base + (long long)u * kWriteThreads;
-        dst[u] = -1;
-        if (i >= total) continue;
-        const int t = (int)(i / per_tok), rem = (int)(i - (long long)t * per_tok);
-        const int h = rem / per_head, c = (rem - h * per_head) * 8;
-        const long long slot = __ldg(p.slots + t);
-        if (slot < 0 || slot >= (long long)p.num_pages * p.ps) continue;
-        const long long page = slot / p.ps;
-        dst[u] = page * p.page_stride + (slot - page * p.ps) * p.token_stride + h * p.head_stride + c;
-        kv[u][0] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token_stride + h * p.k_head_stride + c));
-        kv[u][1] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token_stride + h * p.v_head_stride + c));
-    }
+        for (int u = 0; u < kWriteUnroll; ++u) {
+            const int i = first + u * kWriteThreads;
+            dst[u] = -1;
+            if (i >= n) continue;
+            const int tl = i / per_tok, rem = i - tl * per_tok, t = t0 + tl;
+            const int h = rem >> per_head_log2, c = (rem - (h << per_head_log2)) * 8;
+            const long long slot = __ldg(p.slots + t);
+            if (slot < 0 || slot >= ((long long)p.num_pages << ps_log2)) continue;
+            const long long page = slot >> ps_log2;
+            dst[u] = page * p.page_stride + (slot & (p.ps - 1)) * p.token_stride + h * p.head_stride + c;
+            kv[u][0] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token_stride + h * p.k_head_stride + c));
+            kv[u][1] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token_stride + h * p.v_head_stride + c));
+        }
 #pragma unroll
-    for (int u = 0; u < kWriteUnroll; ++u) {
-        if (dst[u] < 0) continue;
-        *reinterpret_cast<uint4*>(p.k_cache + dst[u]) = kv[u][0];
-        *reinterpret_cast<uint4*>(p.v_cache + dst[u]) = kv[u][1];
+        for (int u = 0; u < kWriteUnroll; ++u) {
+            if (dst[u] < 0) continue;
+            *reinterpret_cast<uint4*>(p.k_cache + dst[u]) = kv[u][0];
+            *reinterpret_cast<uint4*>(p.v_cache + dst[u]) = kv[u][1];
+        }
     }
 }
 
@@ -151,9 +154,10 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& p, int num_sms, cudaStream_t 
 }
 
 cudaError_t launch_paged_write(const PagedWriteArgs& p, cudaStream_t stream) {
-    const long long total = (long long)p.T * p.hkv * (p.d / 8);
-    const long long per = kWriteThreads * kWriteUnroll;
-    k_paged_write<<<(unsigned)((total + per - 1) / per), kWriteThreads, 0, stream>>>(p);
+    const long long per_tok = (long long)p.hkv * (p.d / 8);
+    if (per_tok >= (1ll << 30)) return cudaErrorInvalidValue;
+    const int tokens = (int)std::max(1ll, kWriteThreads * kWriteUnroll / per_tok);
+    k_paged_write<<<(p.T + tokens - 1) / tokens, kWriteThreads, 0, stream>>>(p, tokens);
     return cudaGetLastError();
 }
 
