@@ -78,7 +78,8 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
     p.bidx = bidx;
     p.topk = topk;
     p.bs = bs;
-    p.swin = swin;
+    // a window that no cache outgrows is none (and leaves room for sums with it)
+    p.swin = (long long)swin >= (long long)width * c->page_size ? 0 : swin;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;

@@ -21,6 +21,20 @@
 //   warps 9, 11  MMA issuers, one per stream
 //   warp 10      scheduler: walks the CTA's pieces of work ahead of the others and hands
 //                them over through a ring in shared memory
+//
+// What bounds it.  A chunk of 2048 tokens behind 30720 cached ones (32 query over 8 KV heads,
+// d = 128) takes 945 us, 1.13 PFLOP/s, 68 % of the measured burst rate of a library product of
+// bf16 matrices; called back to back it settles at 0.96 PFLOP/s with the clock (power), 69 %
+// of that product's sustained rate.  Per pair of key tiles (four products of 512 tensor
+// cycles) a stream's chain is about 1900 cycles of softmax (S from TMEM 310, maximum 350,
+// exponentials 1200 of which the special-function unit needs 1024) and 1000 - 1700 of its two
+// products.  Measured and not taken: four softmax warpgroups with two threads a row (1016 us:
+// the two meet once a tile, and TMEM loads queue); every 8th, 4th or 2nd pair of exponentials
+// by polynomial (972 - 1285 us); S in halves of 64 keys (fewer cycles, but Q is read twice a
+// tile and the clock falls: 1010 us); weights formed before the maximum is known (1040 us);
+// one issuer warp for both streams (957 us); the special warps last in the block (1170 us).
+// 16 requests of 3 - 9 tokens on pages of 16: 66 us, 3.4 TB/s; each TMA box of 16 rows costs
+// about as much as one of 32 to issue.
 #include <algorithm>
 #include <type_traits>
 

@@ -219,7 +219,7 @@ struct WalkAll {
         r = owner * per;
         if (per > 1) {                       // the request, among the owner's
             const int end = min(p.R, (owner + 1) * per);
-            for (int base = r;; base += 32) {
+            for (int base = r; base < end; base += 32) {
                 const long long c = cost(p, load(base + lane, end), tpu, lane), ci = scan(c, lane);
                 const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
                 if (hit) {
@@ -232,7 +232,7 @@ struct WalkAll {
             }
         }
         const Req q = request(p, r);
-        for (int base = 0; q.n > tpu; base += 32) {          // its tile of tokens
+        for (int base = 0; q.n > tpu && base * tpu < q.n; base += 32) {   // its tile of tokens
             const int i = base + lane;
             const long long c = i * tpu < q.n ? tile_cost(p, q, i, tpu) : 0, ci = scan(c, lane);
             const unsigned hit = __ballot_sync(0xffffffffu, off < ci);
@@ -253,7 +253,10 @@ struct WalkAll {
             Req q = request(p, r);
             while ((long long)qt * tpu >= q.n) {
                 qt = 0;
-                if (++r == p.R) { r = 0; ++head; }
+                if (++r == p.R) {
+                    r = 0;
+                    if (++head >= p.hkv) return false;   // (lengths that changed under the call)
+                }
                 q = request(p, r);
             }
             const int t = qt * tpu;

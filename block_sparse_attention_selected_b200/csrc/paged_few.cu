@@ -18,6 +18,13 @@
 // odd key tiles; S^T, P^T and (over units) O^T are double-buffered, so that S^T of the next
 // tiles and the epilogue of a unit run under the other products.
 //
+// What bounds it: memory, or what lies before it.  64 requests of one token (4 query heads per
+// KV head, 512 to 32768 keys, 4.36 GB of K and V): 637 us, 6.8 TB/s.  One request of 8192 keys:
+// 20 us, of which the data need 5; the rest is the launch, the scheduler's first piece and the
+// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 69 us,
+// 3.9 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 322 us, 6.6 TB/s, near the 28 bytes a cycle
+// and SM at which the TMA unit takes boxes of 64 rows.
+//
 //   warps 0-7    softmax and epilogue: a warpgroup per stream, one thread per key of the tile
 //                (per value column in the epilogue)
 //   warp 8       TMA producer          warp 10  scheduler

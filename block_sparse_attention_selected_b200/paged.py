@@ -238,7 +238,10 @@ def nsa_sel_paged_attn_fwd(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table
     request r's at rows cu_seqlens[r] .. cu_seqlens[r + 1]; their K/V are in the cache
     already, as the last of its kv_lens[r] tokens.  window_size > 0: each query sees the
     last window_size keys up to its own.  Rows of q behind cu_seqlens[-1] are padding:
-    their outputs are not written.  with_lse=False: None is returned in its place."""
+    their outputs are not written.  with_lse=False: None is returned in its place.
+
+    The call may be captured into a CUDA graph; it then takes its workspace from the graph's
+    memory (pass `workspace` to read the status of a replay with nsa_sel_check_status)."""
     return _attend("nsa_sel_paged_attn_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, (),
                    scale, window_size, out, lse, with_lse, workspace)
 

@@ -412,8 +412,10 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  *   workspace    of nsa_sel_paged_attn_workspace_size() bytes (0: unsupported sizes; else
  *                it depends on head_dim alone), 256-byte aligned, contents arbitrary; calls
  *                that may overlap on the GPU need a workspace each
- * Cache rows that hold no visible key may hold anything, infinities and NaN too.  The
- * scale must be positive and finite.  Other flag bits return NSA_ERR_INVALID_ARG.
+ * Cache rows that hold no visible key may hold anything, infinities and NaN too.  (A
+ * non-finite V row that some query of a request sees can also reach the outputs of that
+ * request's queries of the same KV head that do not see it: 0 times infinity in a shared
+ * product.)  The scale must be positive and finite.  Other flag bits return NSA_ERR_INVALID_ARG.
  * Device-side problems (nsa_sel_check_status): cu_seqlens decreasing or beyond
  * total_tokens, kv_lens beyond the table's row, a used table entry outside [0, num_pages):
  * NSA_ERR_BAD_INDEX, the outputs of that request undefined; no access leaves the cache. */

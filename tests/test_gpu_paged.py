@@ -112,6 +112,30 @@ def test_attend_long_chunks(hq, hkv, q_lens, kv_lens):
     run(make_case(q_lens, kv_lens, hq, hkv, 128, 64, seed=9, pad=5))
 
 
+@pytest.mark.parametrize("q_lens, topk", [([1, 3], 0), ([100, 40], 0), ([400, 300], 0), ([5, 2], 6)])
+def test_window_wider_than_any_cache(q_lens, topk):
+    c = make_case(q_lens, [700, 450], 8, 2, 128, 64, seed=24, topk=topk, poison=False)
+    plain = run(c)
+    for window in (2 ** 31 - 1, 2 ** 31 - 128, 64 * c["table"].shape[1]):
+        got = run(dict(c, window=window))
+        assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("q_len, hq", [(1, 8), (30, 8), (200, 8), (9, 2)])
+def test_a_nan_row_of_q_stays_alone(q_len, hq):
+    c = make_case([q_len, 2], [600, 130], hq, 2, 128, 64, seed=25, poison=False)
+    ref = oracle_of(c)
+    tol, ltol = tolerances(c, ref)
+    bad = (q_len // 2, hq - 1)
+    c["q"][bad] = float("nan")
+    out, lse = (x.double().cpu().numpy() for x in attend(c))
+    rest = np.ones(out.shape[:2], bool)
+    rest[bad] = False
+    assert np.all(np.isnan(out[bad])) and np.isnan(lse[bad[1], bad[0]])
+    assert np.all(np.abs(out - ref[0])[rest] <= tol[rest])
+    assert np.all(np.abs(lse - ref[1]).T[rest] <= ltol.T[rest])
+
+
 def test_attend_many_requests():
     rng = np.random.default_rng(3)
     kv = rng.integers(1, 300, 333)
@@ -190,10 +214,9 @@ def test_select_many_tokens():
 @pytest.mark.parametrize("hq, hkv, topk", [(8, 4, 2), (64, 2, 1), (80, 2, 3), (16, 8, 16)])
 def test_select_many_units(hq, hkv, topk):
     rng = np.random.default_rng(hq)
-    kv = rng.integers(1, 1500, 160)
+    kv = rng.integers(1, 700, 160)
     q = np.minimum(kv, rng.integers(0, 4, 160))
-    for seed in range(2):
-        run(make_case(q.tolist(), kv.tolist(), hq, hkv, 128, 64, seed=50 + seed, topk=topk, pad=1))
+    run(make_case(q.tolist(), kv.tolist(), hq, hkv, 128, 64, seed=50, topk=topk, pad=1))
 
 
 # ------------------------------------------------------- layouts, streams, graphs, status
