@@ -7,6 +7,8 @@ is no fallback: if the library or a CUDA device is missing, calls raise.
 
 Tensors: q [T, hq, 128], k/v [T, hkv, 128] bf16 CUDA; cu_seqlens int32 [nseq+1];
 block_idx int32 [T, hkv, topk] (block numbers local to each sequence, -1 pads).
+
+Serving from a paged K/V cache (the ``nsa_sel_paged_*`` functions): ``paged.py``.
 """
 from __future__ import annotations
 
