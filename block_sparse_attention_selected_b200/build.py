@@ -16,6 +16,8 @@ LIB = os.path.join(HERE, "libnsa_sel.so")
 # the bounds-checking build (-DNSA_SEL_CHECKS): same ABI, every gathered row and K/V
 # block coordinate checked before its copy (nsa_common.cuh)
 LIB_CHECKS = os.path.join(HERE, "libnsa_sel_checks.so")
+# the compiled marshalling of the paged-cache calls (a Python extension module)
+LIB_BIND = os.path.join(HERE, "_paged_bind.so")
 SOURCES = ["api.cu", "invert.cu", "fwd.cu", "merge.cu", "bwd.cu", "select.cu", "bsfa.cu",
            "paged.cu", "paged_attn.cu", "paged_few.cu",
            "paged_api.cu"]
@@ -42,8 +44,33 @@ def _stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_bind(force: bool = False) -> str:
+    """Builds _paged_bind.so, the compiled marshalling of the paged-cache calls (g++ against the
+    headers of the installed Python and torch)."""
+    import sysconfig
+
+    import torch
+    src, header = os.path.join(CSRC, "paged_bind.cpp"), os.path.join(ROOT, "include", "nsa_sel.h")
+    if not force and os.path.exists(LIB_BIND) and \
+            os.path.getmtime(LIB_BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return LIB_BIND
+    base = os.path.dirname(torch.__file__)
+    tmp = LIB_BIND + f".tmp{os.getpid()}"
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         "-isystem", os.path.join(base, "include"),
+         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+         "-I" + sysconfig.get_paths()["include"], src, "-o", tmp,
+         "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, LIB_BIND)
+    return LIB_BIND
+
+
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
-    """Builds libnsa_sel.so (checks=True: the bounds-checking libnsa_sel_checks.so)."""
+    """Builds libnsa_sel.so (checks=True: the bounds-checking libnsa_sel_checks.so), and the
+    binding's compiled module."""
+    build_bind(force)
     lib = LIB_CHECKS if checks else LIB
     if not force and not _stale(lib):
         return lib

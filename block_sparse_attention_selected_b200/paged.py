@@ -28,13 +28,33 @@ __all__ = ["nsa_sel_paged_plan", "nsa_sel_paged_write_kv", "nsa_sel_paged_attn_w
            "nsa_sel_paged_attn_fwd", "nsa_sel_paged_sel_fwd"]
 
 # A decode step makes these calls once per layer on kernels of a few microseconds, so the
-# host path is kept short: each tensor is tested by one expression, and looked at again only
-# to say what is wrong with it; the stream and device queries are those that torch's own
+# host path is kept short: the plain case is marshalled by a small compiled module
+# (csrc/paged_bind.cpp); anything it does not take comes back and is looked at here, where
+# what is wrong gets its name.  The stream and device queries are those that torch's own
 # generated code uses.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 _ELEM = {torch.bfloat16: 0, torch.float16: NSA_F16}
+
+_bind = None   # the compiled module; False where it was not built
+
+
+def _plain(t):
+    """The compiled module, for a call whose first tensor is t."""
+    global _bind
+    if _bind is None:
+        try:
+            from . import _paged_bind
+        except ImportError:
+            _bind = False
+            return _bind
+        lib = load_library()
+        _paged_bind.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.nsa_sel_paged_plan, lib.nsa_sel_paged_write_kv, lib.nsa_sel_paged_attn_fwd,
+            lib.nsa_sel_paged_sel_fwd)))
+        _bind = _paged_bind
+    return _bind and isinstance(t, torch.Tensor) and t.is_cuda and _bind
 
 
 class _Cache(ctypes.Structure):   # nsa_paged_cache_t
@@ -134,6 +154,15 @@ def nsa_sel_paged_plan(new_lens, cached_lens, free_pages, block_table, page_size
     total_tokens: host int, at least the sum of new_lens; rows behind it get slot -1.
     pages_used[0] is what the step needs of free_pages; missing pages are -1 in the table,
     and slots on them -1."""
+    bind = _plain(new_lens)
+    if bind:
+        device = _current_device()
+        got = bind.plan(new_lens, cached_lens, free_pages, block_table, page_size, total_tokens, device,
+                        _raw_stream(device))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            raise NsaError("nsa_sel_paged_plan", got)
     if not isinstance(new_lens, torch.Tensor) or not new_lens.is_cuda:
         raise ValueError("new_lens must be a CUDA tensor")
     index, int32 = new_lens.get_device(), torch.int32
@@ -159,6 +188,14 @@ def nsa_sel_paged_write_kv(k, v, slots, k_cache, v_cache):
 
     k and v may be slices of a wider tensor (a fused QKV projection) whose strides are
     multiples of 8 elements."""
+    bind = _plain(k)
+    if bind:
+        device = _current_device()
+        code = bind.write(k, v, slots, k_cache, v_cache, device, _raw_stream(device))
+        if code == 0:
+            return
+        if code is not None:
+            raise NsaError("nsa_sel_paged_write_kv", code)
     et, _, index = _elem(k, "k")
     ks = _strided(k, "k", et, 3, index)
     vs = _strided(v, "v", et, 3, index)
@@ -192,6 +229,28 @@ def _paged_workspace(T, R, hq, hkv, d, q, stream):
         return q.new_empty(nbytes, dtype=torch.uint8)
     ws = _ws_cache.get((q.device, stream))
     return ws if ws is not None and ws.numel() >= nbytes else get_workspace(nbytes, q.device)
+
+
+def _attend_plain(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, block_idx, block_size, scale,
+                  window_size, out, lse, with_lse, workspace):
+    """(out, lse) by the compiled module, or None."""
+    bind = _plain(q)
+    if not bind:
+        return None
+    device = _current_device()
+    stream = _raw_stream(device)
+    ws = workspace
+    if ws is None:
+        ws = None if _capturing() else _ws_cache.get((q.device, stream))
+        if ws is None:
+            return None
+    got = bind.attend(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, block_idx, block_size, scale,
+                      window_size, out, lse, with_lse, ws, device, stream)
+    if got is None or got.__class__ is tuple:
+        return got
+    if got == 3 and workspace is None:      # the cached workspace is another call's, and smaller
+        return None
+    raise NsaError(fn, got)
 
 
 def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection, scale, window_size,
@@ -242,6 +301,10 @@ def nsa_sel_paged_attn_fwd(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table
 
     The call may be captured into a CUDA graph; it then takes its workspace from the graph's
     memory (pass `workspace` to read the status of a replay with nsa_sel_check_status)."""
+    got = _attend_plain("nsa_sel_paged_attn_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, None, 0,
+                        scale, window_size, out, lse, with_lse, workspace)
+    if got is not None:
+        return got
     return _attend("nsa_sel_paged_attn_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, (),
                    scale, window_size, out, lse, with_lse, workspace)
 
@@ -252,6 +315,10 @@ def nsa_sel_paged_sel_fwd(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
     """Selected-block attention over the paged cache: as nsa_sel_paged_attn_fwd, over the
     keys of the blocks block_idx[t, g, :] (int32 [T, hkv, topk], block numbers local to the
     request's sequence, distinct within a row, -1 pads)."""
+    got = _attend_plain("nsa_sel_paged_sel_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, block_idx,
+                        block_size, scale, window_size, out, lse, with_lse, workspace) if block_idx is not None else None
+    if got is not None:
+        return got
     idx = _packed(block_idx, "block_idx", torch.int32, 3, _elem(q, "q")[2])
     rows, heads, topk = block_idx.shape
     if rows != q.shape[0] or heads != k_cache.shape[2]:

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_selected_b200 as nsa
+from block_sparse_attention_selected_b200 import paged as npaged
 from oracle import paged as po
 from paged_util import DTYPES, make_case, oracle_of, rounded, tolerances
 
@@ -443,7 +444,52 @@ def test_write(T, hkv, d, ps, fused, layout, dtype):
     assert torch.equal(vc.contiguous().view(-1, hkv, d), want_v)
 
 
-def test_binding_refusals_on_the_device():
+@pytest.fixture(params=["compiled", "python"])
+def marshalling(request, monkeypatch):
+    if request.param == "python":
+        monkeypatch.setattr(npaged, "_bind", False)
+    else:
+        assert npaged._plain(torch.zeros(1, device="cuda")), "_paged_bind.so was not built"
+
+
+def test_both_marshallings_agree(monkeypatch):
+    for topk, window, dtype in ((0, 0, "bf16"), (3, 70, "fp16")):
+        c = make_case([1, 30, 0, 2], [300, 200, 5, 64], 6, 2, 64, 32, dtype=dtype, seed=26, topk=topk, pad=3,
+                      window=window)
+        ts = tensors(c)
+        new, old = cuda(np.array([2, 0, 40], np.int32)), cuda(np.array([5, 7, 30], np.int32))
+        free = cuda(np.arange(20, 30, dtype=np.int32))
+        rows = torch.randn(5, 2, 64, device="cuda").to(DTYPES[dtype])
+        slots = torch.tensor([3, -1, 40, 7, 0], device="cuda")
+        got = []
+        for bind in (None, False):
+            monkeypatch.setattr(npaged, "_bind", bind)
+            table = torch.tensor([[1, -1, -1], [2, -1, -1], [3, -1, -1]], dtype=torch.int32, device="cuda")
+            k, v = ts[1].clone().nan_to_num(), ts[2].clone().nan_to_num()
+            nsa.nsa_sel_paged_write_kv(rows, 2 * rows, slots, k, v)
+            lse = torch.zeros(6, c["T"], device="cuda")
+            out = torch.zeros(c["q"].shape, dtype=DTYPES[dtype], device="cuda")
+            a = attend(c, ts, out=out, lse=lse)
+            assert a[0] is out and a[1] is lse
+            n = int(c["cu"][-1])
+            b = attend(c, ts)
+            d = attend(c, ts, with_lse=False)
+            assert d[1] is None and torch.equal(d[0][:n], out[:n])
+            assert torch.equal(b[0][:n], out[:n]) and torch.equal(b[1][:, :n], lse[:, :n])
+            got.append([*nsa.nsa_sel_paged_plan(new, old, free, table, 32, 44), table, k, v, out, lse])
+        for x, y in zip(*got):
+            assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
+
+
+def test_small_cached_workspace_is_grown():
+    nsa.release_workspaces()
+    c = make_case([1], [50], 4, 2, 64, 16, seed=27)
+    nsa.get_workspace(256, "cuda")
+    check(c, attend(c))
+    assert nsa.nsa_sel_check_status() == 0
+
+
+def test_binding_refusals_on_the_device(marshalling):
     c = make_case([2], [50], 4, 2, 64, 16, seed=23)
     q, k, v, cu, kv, table = tensors(c)
     f = nsa.nsa_sel_paged_attn_fwd
