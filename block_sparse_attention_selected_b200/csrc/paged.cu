@@ -29,6 +29,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
     int* pre = plan_smem + p.R + 1;         // [R + 1] fresh pages before request r
     __shared__ long long wsum[2][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    release_dependents();
+    depend();
     const int per = (p.R + kPlanThreads - 1) / kPlanThreads;
     const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
     auto pages = [&](long long tokens) -> int {
@@ -114,6 +116,8 @@ constexpr int kWriteUnroll = 4;
 __global__ void __launch_bounds__(kWriteThreads) k_paged_write(PagedWriteArgs p, int tokens) {
     const int per_head_log2 = 28 - __clz(p.d), per_tok = p.hkv << per_head_log2, ps_log2 = 31 - __clz(p.ps);
     const int t0 = blockIdx.x * tokens, n = min(tokens, p.T - t0) * per_tok;
+    release_dependents();
+    depend();
     for (int first = threadIdx.x; first < n; first += kWriteThreads * kWriteUnroll) {
         uint4 kv[kWriteUnroll][2];
         long long dst[kWriteUnroll];
@@ -151,16 +155,14 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& p, int num_sms, cudaStream_t 
                                              (int)smem);
         if (e != cudaSuccess) return e;
     }
-    k_paged_plan<<<grid, kPlanThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(k_paged_plan, grid, kPlanThreads, smem, stream, p);
 }
 
 cudaError_t launch_paged_write(const PagedWriteArgs& p, cudaStream_t stream) {
     const long long per_tok = (long long)p.hkv * (p.d / 8);
     if (per_tok >= (1ll << 30)) return cudaErrorInvalidValue;
     const int tokens = (int)std::max(1ll, kWriteThreads * kWriteUnroll / per_tok);
-    k_paged_write<<<(p.T + tokens - 1) / tokens, kWriteThreads, 0, stream>>>(p, tokens);
-    return cudaGetLastError();
+    return launch_dependent(k_paged_write, (p.T + tokens - 1) / tokens, kWriteThreads, 0, stream, p, tokens);
 }
 
 }  // namespace nsa

@@ -7,10 +7,36 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../include/nsa_sel.h"
 #include "nsa_common.cuh"
 
 namespace nsa {
+
+// Programmatic dependent launch: the kernels of a step follow one another within
+// microseconds, so each is launched while the one before it still runs, sets itself up, and
+// waits for the end of everything before it (depend()) before it touches memory; it lets the
+// next one do the same from its own start (release_dependents()).
+__device__ __forceinline__ void depend() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void release_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // Host helpers of the C ABI (api.cu).
 nsa_status_t check_device(int* num_sms, nsa_stream_t stream);

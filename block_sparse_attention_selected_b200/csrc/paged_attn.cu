@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    release_dependents();
+    depend();
 
     tc_fence_before();
     __syncthreads();
@@ -520,7 +521,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 // the pieces' columns, eight pieces' loads in flight.
 template <int F16, int D>
 __global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_per_piece) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    release_dependents();
+    depend();
     const PagedAttnArgs& p = P.a;
     const int4 d = P.desc[blockIdx.x];
     if (d.w < 0) return;
@@ -598,25 +600,14 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     cudaError_t e = cudaFuncSetAttribute(k_paged_attn<F16, D, NQ, SEL>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_paged_attn<F16, D, NQ, SEL><<<grid, kPaThreads, smem, stream>>>(P, qmap, kmap, vmap);
-    return cudaGetLastError();
+    return launch_dependent(k_paged_attn<F16, D, NQ, SEL>, grid, kPaThreads, smem, stream, P, qmap, kmap, vmap);
 }
 
-// The merge is launched while the attention kernel still runs and waits for its end
-// (programmatic dependent launch): its launch costs nothing then.
 cudaError_t merge(const Params& P, int f16, int grid, int rows_per_piece, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min(rows_per_piece / 32, (P.a.G * P.tpu + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     auto* kernel = P.a.d == 64 ? (f16 ? k_paged_merge<1, 64> : k_paged_merge<0, 64>)
                                : (f16 ? k_paged_merge<1, 128> : k_paged_merge<0, 128>);
-    return cudaLaunchKernelEx(&cfg, kernel, P, rows_per_piece);
+    const dim3 blocks((unsigned)grid, (unsigned)std::min(rows_per_piece / 32, (P.a.G * P.tpu + 7) / 8));
+    return launch_dependent(kernel, blocks, 256, 0, stream, P, rows_per_piece);
 }
 
 template <int F16, int D>

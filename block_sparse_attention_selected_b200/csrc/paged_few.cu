@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    release_dependents();
+    depend();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -525,8 +526,7 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     cudaError_t e = cudaFuncSetAttribute(k_paged_few<F16, D, SEL>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_paged_few<F16, D, SEL><<<grid, kFewThreads, smem, stream>>>(P, qmap, kmap, vmap);
-    return cudaGetLastError();
+    return launch_dependent(k_paged_few<F16, D, SEL>, grid, kFewThreads, smem, stream, P, qmap, kmap, vmap);
 }
 
 template <int F16, int D>
