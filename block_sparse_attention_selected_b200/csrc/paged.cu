@@ -20,9 +20,10 @@ __device__ __forceinline__ int saturate(long long x) {
 
 // One launch, no pass between blocks: every block scans the request lengths by itself
 // (two int32 reads per request, from L2) into shared memory, then takes its stripe of
-// the fresh pages and of the tokens.  Bound by latency: 4.5 us for 64 requests of one token,
-// 8.6 us for 1000 requests with 130,000 tokens (12 bytes out per token).  A token's slot on a fresh page comes from the free
-// list and not from the table entry that another block may be writing.
+// the fresh pages and of the tokens.  Bound by latency: 3.4 us for 64 requests of one token,
+// 7.1 us for 1000 requests with 130,000 tokens (12 bytes out per token).  A token's slot on a
+// fresh page comes from the free list and not from the table entry that another block may be
+// writing.
 __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
     extern __shared__ int plan_smem[];
     int* cu = plan_smem;                    // [R + 1] tokens before request r
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
     };
     long long tok = 0, fresh = 0;
     for (int r = r0; r < r1; ++r) {
-        const long long old = max(__ldg(p.old_lens + r), 0), add = max(__ldg(p.new_lens + r), 0);
+        const long long old = max(p.old_lens[r], 0), add = max(p.new_lens[r], 0);
         tok += add;
         fresh += pages(old + add) - pages(old);
     }
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
     a -= tok;
     b -= fresh;
     for (int r = r0; r < r1; ++r) {
-        const long long old = max(__ldg(p.old_lens + r), 0), add = max(__ldg(p.new_lens + r), 0);
+        const long long old = max(p.old_lens[r], 0), add = max(p.new_lens[r], 0);
         cu[r] = saturate(a);
         pre[r] = saturate(b);
         if (blockIdx.x == 0) {
@@ -76,15 +77,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
     const int at = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
     for (int j = at; j < pre[p.R]; j += step) {
         const int r = upper_index(pre, p.R, j);   // last r with pre[r] <= j: it has fresh pages
-        const int col = pages(max(__ldg(p.old_lens + r), 0)) + j - pre[r];
-        p.table[(size_t)r * p.table_stride + col] = j < p.num_free ? __ldg(p.free_pages + j) : -1;
+        const int col = pages(max(p.old_lens[r], 0)) + j - pre[r];
+        p.table[(size_t)r * p.table_stride + col] = j < p.num_free ? p.free_pages[j] : -1;
     }
     for (int t = at; t < p.T; t += step) {
         long long slot = -1;
         int pos = 0;
         if (t < cu[p.R]) {
             const int r = upper_index(cu, p.R, t);
-            const int old = max(__ldg(p.old_lens + r), 0);
+            const int old = max(p.old_lens[r], 0);
             const long long at_pos = (long long)old + (t - cu[r]);
             const long long col = at_pos / p.ps;
             int page = -1;
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(PagedPlanArgs p) {
                     page = p.table[(size_t)r * p.table_stride + col];
                 } else {
                     const long long j = (long long)pre[r] + col - have;
-                    if (j < p.num_free) page = __ldg(p.free_pages + j);
+                    if (j < p.num_free) page = p.free_pages[j];
                 }
             }
             pos = saturate(at_pos);
@@ -110,7 +111,8 @@ constexpr int kWriteUnroll = 4;
 
 // Blocks take whole tokens (one at least), threads 16-byte pieces of K and of V, a thread's
 // loads before its first store.  Bound by memory: each row is read once and written once
-// (16384 tokens of 8 heads, 134 MB: 25 us, 5.4 TB/s; with 64-bit divisions 26.6 us).
+// (16384 tokens of 8 heads, 134 MB: 23.4 us, 5.7 TB/s; launched after its predecessor's end
+// 25.0 us, with 64-bit divisions 26.6 us besides).
 // Page and row sizes are powers of two but the number of heads is not: the one division left
 // is of 32-bit numbers.
 __global__ void __launch_bounds__(kWriteThreads) k_paged_write(PagedWriteArgs p, int tokens) {
@@ -128,12 +130,12 @@ __global__ void __launch_bounds__(kWriteThreads) k_paged_write(PagedWriteArgs p,
             if (i >= n) continue;
             const int tl = i / per_tok, rem = i - tl * per_tok, t = t0 + tl;
             const int h = rem >> per_head_log2, c = (rem - (h << per_head_log2)) * 8;
-            const long long slot = __ldg(p.slots + t);
+            const long long slot = p.slots[t];
             if (slot < 0 || slot >= ((long long)p.num_pages << ps_log2)) continue;
             const long long page = slot >> ps_log2;
             dst[u] = page * p.page_stride + (slot & (p.ps - 1)) * p.token_stride + h * p.head_stride + c;
-            kv[u][0] = __ldg(reinterpret_cast<const uint4*>(p.k + t * p.k_token_stride + h * p.k_head_stride + c));
-            kv[u][1] = __ldg(reinterpret_cast<const uint4*>(p.v + t * p.v_token_stride + h * p.v_head_stride + c));
+            kv[u][0] = *reinterpret_cast<const uint4*>(p.k + t * p.k_token_stride + h * p.k_head_stride + c);
+            kv[u][1] = *reinterpret_cast<const uint4*>(p.v + t * p.v_token_stride + h * p.v_head_stride + c);
         }
 #pragma unroll
         for (int u = 0; u < kWriteUnroll; ++u) {

@@ -17,7 +17,8 @@ namespace nsa {
 // Programmatic dependent launch: the kernels of a step follow one another within
 // microseconds, so each is launched while the one before it still runs, sets itself up, and
 // waits for the end of everything before it (depend()) before it touches memory; it lets the
-// next one do the same from its own start (release_dependents()).
+// next one do the same from its own start (release_dependents()).  What such a kernel reads may
+// be written while it is already running, so none of its loads takes the read-only path (__ldg).
 __device__ __forceinline__ void depend() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -33,7 +33,7 @@
 // by polynomial (972 - 1285 us); S in halves of 64 keys (fewer cycles, but Q is read twice a
 // tile and the clock falls: 1010 us); weights formed before the maximum is known (1040 us);
 // one issuer warp for both streams (957 us); the special warps last in the block (1170 us).
-// 16 requests of 3 - 9 tokens on pages of 16: 66 us, 3.4 TB/s; each TMA box of 16 rows costs
+// 16 requests of 3 - 9 tokens on pages of 16: 64 us, 3.5 TB/s; each TMA box of 16 rows costs
 // about as much as one of 32 to issue.
 #include <algorithm>
 #include <type_traits>
@@ -113,11 +113,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_init(&S.drain, 2);
         fence_barrier_init();
     }
-    if (warp == 8) {
-        __syncwarp();
-        tmem_alloc(&S.tmem_base, 512);
-        tmem_relinquish();
-    }
     if (warp == 10 && lane == 0) {
         prefetch_tmap(&qmap);
         prefetch_tmap(&kmap);
@@ -125,7 +120,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     release_dependents();
     depend();
-
+    // (not before: a kernel that this one waits for may need the tensor memory)
+    if (warp == 8) {
+        __syncwarp();
+        tmem_alloc(&S.tmem_base, 512);
+        tmem_relinquish();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

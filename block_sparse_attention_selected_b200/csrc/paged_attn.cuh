@@ -90,13 +90,13 @@ __device__ __forceinline__ void tmem_st16_sync(uint32_t taddr, const float* v) {
 struct Req { int a, n, kv; };
 __device__ __forceinline__ Req request(const PagedAttnArgs& p, int r) {
     Req q;
-    q.a = min(max(__ldg(p.cu + r), 0), p.T);
-    q.n = min(max(__ldg(p.cu + r + 1), q.a), p.T) - q.a;
-    q.kv = min(max(__ldg(p.kv_lens + r), 0), p.table_width * p.ps);
+    q.a = min(max(p.cu[r], 0), p.T);
+    q.n = min(max(p.cu[r + 1], q.a), p.T) - q.a;
+    q.kv = min(max(p.kv_lens[r], 0), p.table_width * p.ps);
     return q;
 }
 __device__ __forceinline__ bool request_ok(const PagedAttnArgs& p, int r) {
-    const int a = __ldg(p.cu + r), b = __ldg(p.cu + r + 1), kv = __ldg(p.kv_lens + r);
+    const int a = p.cu[r], b = p.cu[r + 1], kv = p.kv_lens[r];
     return a >= 0 && b >= a && b <= p.T && kv >= 0 && kv <= p.table_width * p.ps;
 }
 
@@ -279,12 +279,12 @@ struct WalkAll {
 // The last request with cu[r] <= t, by one warp: two rounds of loads for up to 1024 requests.
 __device__ __forceinline__ int find_request(const PagedAttnArgs& p, int t, int lane) {
     const int step = (p.R + 31) / 32, i = lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, i < p.R && __ldg(p.cu + i) <= t);
+    const unsigned m = __ballot_sync(0xffffffffu, i < p.R && p.cu[i] <= t);
     int r = (31 - __clz(m | 1u)) * step;
     if (step == 1) return r;
     const int end = min(r + step, p.R);
     for (int base = r; base < end; base += 32) {
-        const unsigned b = __ballot_sync(0xffffffffu, base + lane < end && __ldg(p.cu + base + lane) <= t);
+        const unsigned b = __ballot_sync(0xffffffffu, base + lane < end && p.cu[base + lane] <= t);
         if (b) r = base + 31 - __clz(b);
         if (b != 0xffffffffu) break;
     }
@@ -307,7 +307,7 @@ struct WalkSel {
     }
     __device__ __forceinline__ bool next(const Params& P, int cta, int grid, int lane, int* list, Piece& k) {
         const PagedAttnArgs& p = P.a;
-        const int t_first = __ldg(p.cu), t_last = __ldg(p.cu + p.R);
+        const int t_first = p.cu[0], t_last = p.cu[p.R];
         for (;;) {
             long long u, u0 = 0, u1 = P.cost_sel;
             if (unit < rounds_end) {
@@ -326,8 +326,8 @@ struct WalkSel {
             const int g = (int)quotient(u, p.T), t = (int)(u - (long long)g * p.T);
             if (t < t_first || t >= t_last) continue;
             const int32_t* row = p.bidx + ((long long)t * p.hkv + g) * p.topk;
-            const int b0 = lane < p.topk ? __ldg(row + lane) : -1;
-            const int b1 = lane + 32 < p.topk ? __ldg(row + lane + 32) : -1;
+            const int b0 = lane < p.topk ? row[lane] : -1;
+            const int b1 = lane + 32 < p.topk ? row[lane + 32] : -1;
             k.r = find_request(p, t, lane);
             const Req q = request(p, k.r);
             if (t < q.a || t >= q.a + q.n) continue;
@@ -536,7 +536,7 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
         nx_live = key >= 0 && key <= k.hi && key + P.box_rows > k.lo;   // a visible key lies in it
         nx_row = key & (p.ps - 1);
         nx_g = k.g;
-        if (nx_live) nx_page = __ldg(p.table + (long long)k.r * p.table_stride + (key >> ps_log2));
+        if (nx_live) nx_page = p.table[(long long)k.r * p.table_stride + (key >> ps_log2)];
         ++j;
         return true;
     };

@@ -20,9 +20,9 @@
 //
 // What bounds it: memory, or what lies before it.  64 requests of one token (4 query heads per
 // KV head, 512 to 32768 keys, 4.36 GB of K and V): 637 us, 6.8 TB/s.  One request of 8192 keys:
-// 20 us, of which the data need 5; the rest is the launch, the scheduler's first piece and the
-// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 69 us,
-// 3.9 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 322 us, 6.6 TB/s, near the 28 bytes a cycle
+// 18 us, of which the data need 5; the rest is the scheduler's first piece and the
+// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 68 us,
+// 4.0 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 322 us, 6.6 TB/s, near the 28 bytes a cycle
 // and SM at which the TMA unit takes boxes of 64 rows.
 //
 //   warps 0-7    softmax and epilogue: a warpgroup per stream, one thread per key of the tile
@@ -136,11 +136,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_init(&S.drain, 2);
         fence_barrier_init();
     }
-    if (warp == 8) {
-        __syncwarp();
-        tmem_alloc(&S.tmem_base, kCols);
-        tmem_relinquish();
-    }
     if (warp == 10 && lane == 0) {
         prefetch_tmap(&qmap);
         prefetch_tmap(&kmap);
@@ -148,6 +143,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     release_dependents();
     depend();
+    // (not before: a kernel that this one waits for may need the tensor memory)
+    if (warp == 8) {
+        __syncwarp();
+        tmem_alloc(&S.tmem_base, kCols);
+        tmem_relinquish();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

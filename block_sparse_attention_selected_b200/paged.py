@@ -281,7 +281,11 @@ def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection
         lse = q.new_empty((hq, T), dtype=torch.float32)
         lse_to = lse.data_ptr()
     stream = _raw_stream(index)
-    ws = workspace if workspace is not None else _paged_workspace(T, R, hq, cshape[2], d, q, stream)
+    if workspace is not None:
+        ws = workspace
+        _packed(ws, "workspace", torch.uint8, 1, index)
+    else:
+        ws = _paged_workspace(T, R, hq, cshape[2], d, q, stream)
     _call(fn, index, q.data_ptr(), qs[0], qs[1], T, hq, ctypes.byref(cache), cu, kv, R, *table, *selection,
           d ** -0.5 if scale is None else float(scale), int(window_size), to, lse_to, ws.data_ptr(), ws.numel(),
           stream, flag)

@@ -344,6 +344,44 @@ def test_a_step_captured_and_replayed_with_new_lengths():
         check(dict(c, idx=idx.cpu().numpy()), b)
 
 
+def test_calls_that_read_what_the_call_before_wrote():
+    # each kernel starts under the one before it: 25 steps of two layers whose inputs are the
+    # outputs of the calls just before give what they give with a wait after every call
+    ps, R, hq, hkv, d, steps = 16, 3, 4, 2, 64, 25
+    rng = np.random.default_rng(22)
+    q0, k0, v0 = (cuda(rng.standard_normal((steps, R, h, d)).astype(np.float32)).bfloat16() for h in (hq, hkv, hkv))
+    one = torch.ones(R, dtype=torch.int32, device="cuda")
+    idx = torch.tensor([0, -1, 1], dtype=torch.int32, device="cuda").expand(R, hkv, 3).contiguous()
+
+    def go(wait):
+        table = torch.full((R, 8), -1, dtype=torch.int32, device="cuda")
+        free = torch.arange(60, dtype=torch.int32, device="cuda")
+        kc, vc = (torch.zeros(2, 60, ps, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        old = torch.full((R,), 2 * ps - 13, dtype=torch.int32, device="cuda")
+        table[:, :2] = 50 + torch.arange(2 * R, device="cuda").view(R, 2)
+        seen = []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            cu, old, slots, pos, used = nsa.nsa_sel_paged_plan(one, old, free[R * (i // ps):], table, ps, R)
+            wait()
+            x = [q0[i], k0[i], v0[i]]
+            for layer in range(2):
+                nsa.nsa_sel_paged_write_kv(x[1], x[2], slots, kc[layer], vc[layer])
+                wait()
+                out, lse = nsa.nsa_sel_paged_attn_fwd(x[0], kc[layer], vc[layer], cu, old, table)
+                wait()
+                out, sel_lse = nsa.nsa_sel_paged_sel_fwd(out, kc[layer], vc[layer], cu, old, table, idx, 64)
+                wait()
+                seen += [slots, pos, used, out, lse, sel_lse]
+                x = [out, out[:, :hkv], out[:, hkv:]]
+        torch.cuda.synchronize()
+        assert nsa.nsa_sel_check_status() == 0
+        return seen + [table, kc, vc, old]
+
+    for x, y in zip(go(lambda: None), go(torch.cuda.synchronize), strict=True):
+        assert torch.equal(x, y)
+
+
 def test_bad_pages_and_lengths_are_reported():
     c = make_case([1, 3], [200, 100], 8, 2, 128, 64, seed=22, poison=False)
     ref = oracle_of(c)
@@ -487,6 +525,22 @@ def test_small_cached_workspace_is_grown():
     nsa.get_workspace(256, "cuda")
     check(c, attend(c))
     assert nsa.nsa_sel_check_status() == 0
+
+
+def test_refused_workspaces(marshalling):
+    c = make_case([2], [50], 4, 2, 64, 16, seed=24)
+    args = tensors(c)
+    nbytes = nsa.nsa_sel_paged_attn_workspace_size(2, 1, 4, 2, 64)
+    good = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    for bad in [torch.empty(nbytes, dtype=torch.uint8), good[None], torch.empty(2 * nbytes, dtype=torch.uint8,
+                                                                             device="cuda")[::2]]:
+        with pytest.raises(ValueError):
+            nsa.nsa_sel_paged_attn_fwd(*args, workspace=bad)
+    with pytest.raises(TypeError):
+        nsa.nsa_sel_paged_attn_fwd(*args, workspace=good.view(torch.int32))
+    with pytest.raises(nsa.NsaError):     # not aligned
+        nsa.nsa_sel_paged_attn_fwd(*args, workspace=torch.empty(nbytes + 16, dtype=torch.uint8, device="cuda")[16:])
+    nsa.nsa_sel_paged_attn_fwd(*args, workspace=good)
 
 
 def test_binding_refusals_on_the_device(marshalling):
