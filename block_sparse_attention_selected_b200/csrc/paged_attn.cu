@@ -23,8 +23,8 @@
 //                them over through a ring in shared memory
 //
 // What bounds it.  A chunk of 2048 tokens behind 30720 cached ones (32 query over 8 KV heads,
-// d = 128) takes 945 us, 1.13 PFLOP/s, 68 % of the measured burst rate of a library product of
-// bf16 matrices; called back to back it settles at 0.96 PFLOP/s with the clock (power), 69 %
+// d = 128) takes 945 us (920 - 1040 on other GPUs: the clock), 1.13 PFLOP/s, 68 % of the measured
+// burst rate of a library product of bf16 matrices; called back to back it settles at 0.96 PFLOP/s with the clock (power), 69 %
 // of that product's sustained rate.  Per pair of key tiles (four products of 512 tensor
 // cycles) a stream's chain is about 1900 cycles of softmax (S from TMEM 310, maximum 350,
 // exponentials 1200 of which the special-function unit needs 1024) and 1000 - 1700 of its two
