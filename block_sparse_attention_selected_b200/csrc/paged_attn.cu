@@ -52,7 +52,7 @@ struct alignas(1024) PaSmem {
     static constexpr int kHalves = D / 64;
     static constexpr int kStages = D == 128 ? 4 : 8;
     uint8_t q[2][kHalves][kRegion];           // NQ = 2: the unit's two tiles; NQ = 1: two units
-    uint8_t kv[kStages][kHalves][kRegion];    // K and V tiles in the order the issuer uses them
+    uint8_t kv[kStages][kHalves * kRegion];   // K and V tiles in the order the issuer uses them
     float2 xch[2][2][128];                    // NQ = 1: [unit parity][stream][row] (m, l)
     Piece ring[kRing];                        // the scheduler's pieces, in order
     int list[kRing][kMaxTopk];                // selected blocks: the valid ones of each
@@ -151,14 +151,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const uint32_t elected = elect_one();
         constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
         constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
+        using Kv = Tile<D>;
         constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+        constexpr uint32_t kStepU = 2 * Kv::kGroupU;     // 16 keys of V
         constexpr int step = NQ == 2 ? 1 : 2;
         auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
         const int st = (int)u(warp == 9 ? 0u : 1u);
         const uint32_t tS = u(tmem + st * 128u), tO = u(tmem + 256u + st * 128u);
         const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
-        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024));
-        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), kRegion, 1024));
+        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 16, 0));
+        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 1024, 0));
         uint64_t *const s_full = &S.s_full[st], *const p_half = &S.p_half[st], *const p_full = &S.p_full[st];
         uint64_t *const o_full = &S.o_full[st],
                  *const o_empty = &S.o_empty[st];
@@ -207,8 +209,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             if (rows_s) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2);
-                    mma_ss_e(tS, a0 + off, b0 + off, kIdescS, x > 0 ? 1u : 0u, elected);
+                    mma_ss_hi(tS, a0 + (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2), kSw128Sbo1024DescHi,
+                              b0 + (uint32_t)((x >> 2) * Kv::kHalfU + (x & 3) * 2), Kv::kDescHi, kIdescS,
+                              x > 0 ? 1u : 0u, elected);
                 }
             }
             mma_commit_e(s_full, elected);
@@ -255,13 +258,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             if (!full) {
                 // clear the rows of the used 16-key steps that nobody may see (NQ = 2: both
                 // issuers do, each before its own products)
-                uint8_t* v = S.kv[stg][0];
-                auto clear = [&](int from, int to) {
-                    for (int r = from; r < to; ++r)
-                        if (lane < 8 * kHalves)
-                            *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                };
+                uint8_t* v = S.kv[stg];
+                auto clear = [&](int from, int to) { clear_rows<D>(v, from, to, lane); };
                 if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
                 if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
                 fence_async_smem();
@@ -276,20 +274,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             if (rows_o && full) {         // the first 64 keys while the rows work on the others
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, x == 0 ? acc : 1u, elected);
+                    mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, x == 0 ? acc : 1u, elected);
             }
             if (!(ok = wait(p_full, items & 1))) break;
             tc_fence_after();
             if (rows_o && full) {
 #pragma unroll
-                for (int x = 4; x < 8; ++x) mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, 1u, elected);
+                for (int x = 4; x < 8; ++x)
+                    mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, 1u, elected);
             } else if (rows_o) {
 #pragma unroll 1
                 for (int x = 0; x < kTileKeys / 16; ++x) {
                     const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
                                            : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
                     if (use) {
-                        mma_ts_e(tO, tS + x * 8u, b0 + x * 128u, kIdescO, acc, elected);
+                        mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, acc, elected);
                         acc = 1u;
                     }
                 }
@@ -586,7 +585,7 @@ bool encode(CUtensorMap* map, bool f16, int rank, const void* base, const cuuint
             const cuuint64_t* strides, const cuuint32_t* box) {
     auto enc = get_encode_fn();
     if (!enc) return false;
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -657,7 +656,13 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     const bool two = !few && !sel && two_tiles(a);
     P.tpt = sel ? 1 : (few ? kFewRows : kTileRows) / a.G;
     P.tpu = two ? 2 * P.tpt : P.tpt;
-    P.box_rows = std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys);
+    // A box is the keys of a page that a tile or block holds, in one dimension of 8-key groups
+    // over all pages.  Pages that are no multiple of 8 keys apart go by boxes of 8 keys.
+    const long long group = 8 * a.token_stride;
+    const bool whole = group > 0 && (a.num_pages == 1 || (a.page_stride % group == 0 && a.page_stride / group >= a.ps / 8));
+    const long long per_page = !whole ? 0 : a.num_pages == 1 ? a.ps / 8 : a.page_stride / group;
+    P.page_groups = (per_page + 1) * (a.num_pages + 1ll) < (1ll << 31) ? (int)per_page : 0;
+    P.box_rows = P.page_groups ? std::min(a.ps, sel ? std::min(a.bs, kTileKeys) : kTileKeys) : 8;
     int grid = std::min(num_sms, kMaxStatusCtas);
     if (sel) {
         P.cost_sel = (a.topk * a.bs + kTileKeys - 1) / kTileKeys + kUnitCost;
@@ -671,13 +676,18 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     };
     const cuuint64_t qstr[2] = {stride(a.q_head_stride, a.hq), stride(a.q_token_stride, a.T)};
     const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)P.tpt};
-    const cuuint64_t kdims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.hkv, (cuuint64_t)a.ps,
-                                 (cuuint64_t)a.num_pages};
-    const cuuint64_t kstr[3] = {stride(a.head_stride, a.hkv), stride(a.token_stride, a.ps),
-                                stride(a.page_stride, a.num_pages)};
-    const cuuint32_t kbox[4] = {64, 1, (cuuint32_t)P.box_rows, 1};
-    if (!encode(&qmap, f16, 3, a.q, qdims, qstr, qbox) || !encode(&kmap, f16, 4, a.k, kdims, kstr, kbox) ||
-        !encode(&vmap, f16, 4, a.v, kdims, kstr, kbox))
+    // (64 columns, keys, halves, 8-key groups, heads) or (64 columns, keys, halves, heads, pages)
+    const bool by_group = P.page_groups > 0;
+    const cuuint64_t halves = a.d / 64, heads = a.hkv, pages = a.num_pages;
+    const cuuint64_t groups = (pages - 1) * P.page_groups + a.ps / 8;
+    const cuuint64_t kdims[5] = {64, (cuuint64_t)(by_group ? 8 : a.ps), halves, by_group ? groups : heads,
+                                 by_group ? heads : pages};
+    const cuuint64_t head_bytes = stride(a.head_stride, a.hkv);
+    const cuuint64_t kstr[4] = {stride(a.token_stride, a.ps), 128, by_group ? (cuuint64_t)group * 2 : head_bytes,
+                                by_group ? head_bytes : stride(a.page_stride, a.num_pages)};
+    const cuuint32_t kbox[5] = {64, 8, (cuuint32_t)halves, by_group ? (cuuint32_t)P.box_rows / 8 : 1, 1};
+    if (!encode(&qmap, f16, 3, a.q, qdims, qstr, qbox) || !encode(&kmap, f16, 5, a.k, kdims, kstr, kbox) ||
+        !encode(&vmap, f16, 5, a.v, kdims, kstr, kbox))
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (few)

@@ -27,6 +27,17 @@ namespace nsa {
 
 constexpr int kTileKeys = 128;
 constexpr int kRegion = kTileKeys * 128;     // bytes of 128 rows x 64 columns
+// A K or V tile in shared memory: groups of 8 keys, in each the 64-column halves one after the
+// other (8 rows of 128 bytes, 128-byte swizzle).  A box of whole rows is then contiguous, so that
+// a page takes one TMA load; a box costs the TMA unit about 50 cycles next to its bytes (pages of
+// 16, a box per half: 18 bytes a cycle and SM; pages of 64: 28).
+template <int D>
+struct Tile {
+    static constexpr uint32_t kGroup = D * 16;                 // bytes of 8 keys
+    static constexpr uint32_t kGroupU = kGroup >> 4, kHalfU = 1024 >> 4;   // descriptor units
+    // the upper word of the descriptors (those of Q and P: kSw128Sbo1024DescHi)
+    static constexpr uint32_t kDescHi = (kGroup >> 4) | 1u << 14 | 2u << 29;
+};
 constexpr int kUnitCost = 1;                 // a unit's prologue and epilogue, in key tiles
 constexpr int kMergeCost = 6;                // writing and joining partial results, in key tiles
 constexpr float kLazy = 8.f;
@@ -49,20 +60,55 @@ struct Params {
     PagedAttnArgs a;
     int tpt;            // tokens per tile of query rows
     int tpu;            // tokens per unit
-    int box_rows;       // rows of one K / V box
+    int box_rows;       // keys of one K / V box
+    int page_groups;    // > 0: places of a page in the maps' dimension of 8-key groups; 0: the maps
+                        // have dimensions of keys and pages, and boxes of 8 keys
     int cost_sel;       // selected blocks: places of a unit on the line
     float* part_o;      // [pieces][NQ * 128][D]
     float2* part_ml;    // [pieces][NQ * 128] (m, l)
     int4* desc;         // [grid] unit left open by CTA c: (token, ntok, g, last CTA) or last = -1
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                            int c1, int c2, int c3) {
+// (whole rows: the coordinates of the columns are 0)
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c3,
+                                              int c4) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c3), "r"(c4)
         : "memory");
+}
+// mma_ss_e and mma_ts_e with the upper words of the operands' descriptors
+__device__ __forceinline__ void mma_ss_hi(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\t"
+        "mov.b64 db, {%2, %7};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected), "r"(a_hi), "r"(b_hi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_hi(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi,
+                                          uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "mov.b64 db, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected), "r"(b_hi)
+        : "memory");
+}
+// Clears rows [from, to) of a tile, by one warp.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int lane) {
+    for (int r = from; r < to; ++r)
+        if (lane < D / 8)
+            *reinterpret_cast<uint4*>(tile + (r >> 3) * Tile<D>::kGroup + (lane >> 3) * 1024 + (r & 7) * 128 +
+                                      (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 // 16 consecutive fp32 columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, float* v) {
@@ -497,12 +543,11 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
                                         const CUtensorMap* kmap, const CUtensorMap* vmap, int lane) {
     constexpr int kHalves = Smem::kHalves, kRun = Stages::kRun;
     const PagedAttnArgs& p = P.a;
-    const int boxes = kTileKeys / P.box_rows;      // per tile and 64-column half
-    const int box = lane / kHalves, half = lane - box * kHalves;
-    const uint32_t box_bytes = (uint32_t)P.box_rows * 128u;
+    const int boxes = kTileKeys / P.box_rows;      // per tile: at most 16
+    const uint32_t box_bytes = (uint32_t)P.box_rows * (kHalves * 128u);
     // (page and block sizes are powers of two)
     const int ps_log2 = 31 - __clz(p.ps), bs_log2 = SEL ? 31 - __clz(p.bs) : 0;
-    const int c0 = box * P.box_rows;               // this lane's box: its first key in the tile
+    const int c0 = lane * P.box_rows;              // this lane's box: its first key in the tile
     int tk = 0, tv = 0;         // K and V tiles loaded
     int units = 0;              // units whose Q was loaded
     int at = -1;                // piece of the next K tile
@@ -525,7 +570,7 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
         if (!more) return true;
         const Piece& k = S.ring[at % kRing];
         int key = -1;
-        if (lane < boxes * kHalves) {
+        if (lane < boxes) {
             if (!SEL) {
                 key = (k.tile0 + j) * kTileKeys + c0;
             } else {
@@ -540,17 +585,17 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
         ++j;
         return true;
     };
-    // the tiles whose K is on its way and whose V is not
-    int page_q[kRun] = {}, row_q[kRun] = {}, g_q[kRun] = {};
+    // the tiles whose K is on its way and whose V is not: the boxes' coordinates
+    int key_q[kRun] = {}, group_q[kRun] = {}, last_q[kRun] = {};
     unsigned mask_q[kRun] = {};
     int pending = 0;
-    auto load = [&](const CUtensorMap* map, typename Stages::At to, int page, int row, int g, unsigned mask) -> bool {
+    auto load = [&](const CUtensorMap* map, typename Stages::At to, int c1, int c3, int c4, unsigned mask) -> bool {
         const int stg = to.stage;
         if (!wait(&S.kv_empty[stg], to.phase ^ 1)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[stg], (uint32_t)__popc(mask) * box_bytes);
         __syncwarp();
         if (mask >> lane & 1)
-            tma_load_4d(S.kv[stg][half] + box * box_bytes, map, &S.kv_full[stg], half * 64, g, row, page);
+            tma_load_rows(S.kv[stg] + lane * box_bytes, map, &S.kv_full[stg], c1, c3, c4);
         return true;
     };
     ok = advance();
@@ -577,28 +622,31 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
                 nx_page = p.num_pages;
             }
             const unsigned mask = __ballot_sync(0xffffffffu, nx_live);
+            const int c1 = P.page_groups ? 0 : nx_row;
+            const int c3 = P.page_groups ? nx_page * P.page_groups + (nx_row >> 3) : nx_g;
+            const int c4 = P.page_groups ? nx_g : nx_page;
 #pragma unroll
             for (int i = 0; i < kRun; ++i)
                 if (i == pending) {
-                    page_q[i] = nx_page;
-                    row_q[i] = nx_row;
-                    g_q[i] = nx_g;
+                    key_q[i] = c1;
+                    group_q[i] = c3;
+                    last_q[i] = c4;
                     mask_q[i] = mask;
                 }
-            if (!(ok = load(kmap, Stages::k(tk), nx_page, nx_row, nx_g, mask))) break;
+            if (!(ok = load(kmap, Stages::k(tk), c1, c3, c4, mask))) break;
             ++tk;
             ++pending;
             if (!(ok = advance())) break;
             if (pending < kRun) continue;
         }
         if (pending == 0) break;
-        if (!(ok = load(vmap, Stages::v(tv), page_q[0], row_q[0], g_q[0], mask_q[0]))) break;
+        if (!(ok = load(vmap, Stages::v(tv), key_q[0], group_q[0], last_q[0], mask_q[0]))) break;
         ++tv;
 #pragma unroll
         for (int i = 0; i + 1 < kRun; ++i) {
-            page_q[i] = page_q[i + 1];
-            row_q[i] = row_q[i + 1];
-            g_q[i] = g_q[i + 1];
+            key_q[i] = key_q[i + 1];
+            group_q[i] = group_q[i + 1];
+            last_q[i] = last_q[i + 1];
             mask_q[i] = mask_q[i + 1];
         }
         --pending;

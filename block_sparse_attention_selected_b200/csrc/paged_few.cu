@@ -48,7 +48,7 @@ struct alignas(1024) FewSmem {
     static constexpr int kAhead = 2;          // S^T tiles of a stream ahead of its P V
     uint8_t q[2][kHalves][N * 128];           // [unit parity][64 columns][row]
     uint8_t pt[2][2][2][N * 128];             // [stream][buffer][64 keys][row]
-    uint8_t kv[kStages][kHalves][kRegion];
+    uint8_t kv[kStages][kHalves * kRegion];
     Piece ring[kRing];
     int list[kRing][kMaxTopk];
     float wmax[2][4][N];                      // [stream][warp][row] a tile's maxima
@@ -164,16 +164,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const uint32_t elected = elect_one();
         constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, N, false, false);
         constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, N, true, false);
-        constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+        using Kv = Tile<D>;
+        constexpr uint32_t kTileU = kHalves * kRegion >> 4;
+        constexpr uint32_t kStepU = 2 * Kv::kGroupU;     // 16 keys of V
         constexpr uint32_t kSmallU = (N * 128) >> 4;     // 64 columns of Q, 64 keys of P^T
         auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
         const int st = (int)u(warp == 9 ? 0u : 1u);
         const uint32_t tS = u(tmem + st * 2u * N), tO = u(tmem + 4u * N + st * 2u * N);
         const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
-        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), 16, 1024));
+        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 16, 0));
         // V^T: 128 rows are two 64-column halves; with D = 64 the half is read twice and
         // lanes 64 - 127 of O^T repeat lanes 0 - 63
-        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0][0]), D == 128 ? kRegion : 0, 1024));
+        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), D == 128 ? 1024 : 0, 0));
         const uint32_t p_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.pt[st][0][0]), 16, 1024));
         int at_s = -1, js = 0, js_end = 0, base_s = 0, count_s = 0, units_s = 0, items_s = 0;
         int at_o = -1, jo = 0, jo_end = 0, base_o = 0, count_o = 0, items_o = 0, sums = 0;
@@ -214,8 +216,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < D / 16; ++x)
-                mma_ss_e(d0, a0 + (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2),
-                         b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2), kIdescS, x > 0 ? 1u : 0u, elected);
+                mma_ss_hi(d0, a0 + (uint32_t)((x >> 2) * Kv::kHalfU + (x & 3) * 2), Kv::kDescHi,
+                          b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2), kSw128Sbo1024DescHi, kIdescS, x > 0 ? 1u : 0u,
+                          elected);
             mma_commit_e(&S.s_full[st][b], elected);
             mma_commit_e(&S.kv_empty[stg], elected);
             ++items_s;
@@ -259,13 +262,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             const bool full = l0 == 0 && h0 == 63 && l1 == 64 && h1 == 127;
             if (!full) {   // clear the rows of the used 16-key steps that nobody may see
-                uint8_t* v = S.kv[stg][0];
-                auto clear = [&](int from, int to) {
-                    for (int r = from; r < to; ++r)
-                        if (lane < 8 * kHalves)
-                            *reinterpret_cast<uint4*>(v + (lane >> 3) * kRegion + r * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                };
+                uint8_t* v = S.kv[stg];
+                auto clear = [&](int from, int to) { clear_rows<D>(v, from, to, lane); };
                 if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
                 if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
                 fence_async_smem();
@@ -284,16 +282,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (full) {
 #pragma unroll
                     for (int x = 0; x < kTileKeys / 16; ++x)
-                        mma_ss_e(d0, a0 + x * 128u, b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2), kIdescO,
-                                 x == 0 ? acc : 1u, elected);
+                        mma_ss_hi(d0, a0 + x * kStepU, Kv::kDescHi, b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2),
+                                  kSw128Sbo1024DescHi, kIdescO, x == 0 ? acc : 1u, elected);
                 } else {
 #pragma unroll 1
                     for (int x = 0; x < kTileKeys / 16; ++x) {
                         const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
                                                : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
                         if (use) {
-                            mma_ss_e(d0, a0 + x * 128u, b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2), kIdescO,
-                                     acc, elected);
+                            mma_ss_hi(d0, a0 + x * kStepU, Kv::kDescHi,
+                                      b0 + (uint32_t)((x >> 2) * kSmallU + (x & 3) * 2), kSw128Sbo1024DescHi, kIdescO, acc,
+                                      elected);
                             acc = 1u;
                         }
                     }

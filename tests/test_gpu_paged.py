@@ -243,6 +243,56 @@ def test_attend_strided_inputs():
         assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
 
 
+@pytest.mark.parametrize("ps", [16, 64, 256])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,topk", [([2, 1, 0, 4], 0), ([40, 1, 9, 130], 0), ([3, 1, 12, 7], 5)],
+                         ids=["few", "chunks", "selected"])
+def test_attend_cache_strides(q_lens, topk, d, ps):
+    # pages at a distance that is no multiple of 8 tokens, tokens and heads with gaps between
+    # them, heads before tokens, K and V side by side: the same bits as packed caches
+    c = make_case(q_lens, [300, 129, 17, 513], 8, 2, d, ps, seed=28, topk=topk)
+    q, k, v, cu, kv, table = tensors(c)
+    plain = run(c)
+    pages, hkv = k.shape[0], k.shape[2]
+
+    def placed(shape, size, strides):
+        out = []
+        for x in (k, v):
+            y = torch.full((size,), float("nan"), dtype=x.dtype, device="cuda").as_strided(shape, strides)
+            y.copy_(x)
+            out.append(y)
+        return out
+
+    shape, tok = tuple(k.shape), hkv * d
+    gaps = [
+        placed(shape, pages * (ps * tok + 8), (ps * tok + 8, tok, d, 1)),                  # after a page
+        placed(shape, pages * (ps * tok + 4 * tok), (ps * tok + 4 * tok, tok, d, 1)),      # half a group
+        placed(shape, pages * (ps + 8) * tok, ((ps + 8) * tok, tok, d, 1)),                # a whole one
+        placed(shape, pages * ps * (tok + 16), (ps * (tok + 16), tok + 16, d, 1)),         # after a token
+        placed(shape, pages * ps * hkv * (d + 8), (ps * hkv * (d + 8), hkv * (d + 8), d + 8, 1)),
+        placed(shape, pages * ps * tok, (ps * tok, d, ps * d, 1)),                         # heads first
+        placed(shape, pages * hkv * (ps * d + 8), (hkv * (ps * d + 8), d, ps * d + 8, 1)),
+        placed(shape, pages * ps * tok, (d, pages * tok, pages * d, 1)),                   # pages last
+    ]
+    both = torch.stack([k, v], 3)
+    gaps.append((both[:, :, :, 0], both[:, :, :, 1]))
+    for kc, vc in gaps:
+        got = attend(c, (q, kc, vc, cu, kv, table))
+        n = int(c["cu"][-1])
+        assert nsa.nsa_sel_check_status() == 0
+        assert torch.equal(got[0][:n], plain[0][:n]) and torch.equal(got[1][:, :n], plain[1][:, :n])
+
+
+def test_attend_a_cache_of_one_page():
+    for stride in (1, 8, 1 << 40):
+        c = make_case([3], [200], 8, 2, 128, 256, seed=29)
+        q, k, v, cu, kv, table = tensors(c)
+        k, v = (x[int(c["table"][0, 0]):][:1] for x in (k, v))
+        k, v = (x.as_strided(x.shape, (8 * stride, *x.stride()[1:])) for x in (k, v))
+        check(c, nsa.nsa_sel_paged_attn_fwd(q, k, v, cu, kv, torch.zeros_like(table), scale=c["scale"]))
+        assert nsa.nsa_sel_check_status() == 0
+
+
 def test_attend_without_lse_and_repeats_bit_for_bit():
     for topk in (0, 6):
         c = make_case([1, 90, 1, 4], [3000, 500, 64, 1000], 8, 2, 128, 64, seed=17, topk=topk)
