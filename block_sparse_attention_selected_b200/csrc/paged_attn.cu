@@ -33,8 +33,8 @@
 // by polynomial (972 - 1285 us); S in halves of 64 keys (fewer cycles, but Q is read twice a
 // tile and the clock falls: 1010 us); weights formed before the maximum is known (1040 us);
 // one issuer warp for both streams (957 us); the special warps last in the block (1170 us).
-// 16 requests of 3 - 9 tokens on pages of 16: 64 us, 3.5 TB/s; each TMA box of 16 rows costs
-// about as much as one of 32 to issue.
+// 16 requests of 3 - 9 tokens on pages of 16: 56 us, 4.0 TB/s; long caches 5.8 TB/s (pages of 64:
+// 6.6), bound by the issue of TMA boxes, one a page.
 #include <algorithm>
 #include <type_traits>
 
@@ -623,8 +623,8 @@ bool two_tiles(const PagedAttnArgs& p) { return (long long)p.T * p.G > 128ll * p
 
 // The transposed products for units of few query rows: up to kFewRows rows of a token's query
 // heads (selected blocks), or of a request's new tokens on average.  Measured against tiles of
-// 128 rows: 64 requests of one token, 4 rows a unit, 637 against 685 us; 8 rows, 16 selected
-// blocks, 68 against 71 us, a chunk of 512 such tokens 322 against 390 us.  The same kernel
+// 128 rows: 64 requests of one token, 4 rows a unit, 634 against 662 us; 8 rows, 16 selected
+// blocks, 67 against 67 us, a chunk of 512 such tokens 305 against 349 us.  The same kernel
 // with 32 rows lost (16 requests of 3 - 9 tokens, 24 rows on average: 92 against 66 us): its
 // Q and P^T leave room for two thirds of the K / V stages only.
 bool few_rows(const PagedAttnArgs& p) {
@@ -666,7 +666,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     int grid = std::min(num_sms, kMaxStatusCtas);
     if (sel) {
         P.cost_sel = (a.topk * a.bs + kTileKeys - 1) / kTileKeys + kUnitCost;
-        grid = (int)std::min<long long>(grid, (long long)a.T * a.hkv * P.cost_sel);
+        const long long units = (long long)a.T * a.hkv, line = units * P.cost_sel;
+        grid = (int)std::min<long long>(grid, line);
+        // (512 units of 8 tiles on 148 SMs: 63 us whole, 67 us cut; 8 such units: cut)
+        P.whole_sel = (units + grid - 1) / grid * P.cost_sel <= (line + grid - 1) / grid + kMergeCost;
     }
     CUtensorMap qmap, kmap, vmap;
     const cuuint64_t qdims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.hq, (cuuint64_t)a.T};
@@ -699,8 +702,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
         e = f16 ? dispatch<1, 128>(P, two, grid, qmap, kmap, vmap, stream)
                 : dispatch<0, 128>(P, two, grid, qmap, kmap, vmap, stream);
     if (e != cudaSuccess) return e;
-    // nothing is cut where whole units fill the rounds
-    if (sel && (long long)a.T * a.hkv % grid == 0) return cudaSuccess;
+    if (P.whole_sel) return cudaSuccess;      // nothing is cut
     return merge(P, f16, grid, two ? 256 : 128, stream);
 }
 

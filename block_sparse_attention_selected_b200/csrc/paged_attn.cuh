@@ -12,7 +12,7 @@
 //   selected blocks  a unit is one token and walks the list of its valid blocks.  Units go
 //                    round the CTAs, all tokens of a KV head before the next head, so that
 //                    the tokens of a chunk find the head's blocks in L2; the units that do
-//                    not fill a last round form a line as above.
+//                    not fill a last round form a line as above, by the same rule.
 //
 // Keys that no row of a unit may see are never read into a product: their pages are not
 // loaded, and the issuers leave out the 16-key steps of P V without a visible key and
@@ -64,6 +64,7 @@ struct Params {
     int page_groups;    // > 0: places of a page in the maps' dimension of 8-key groups; 0: the maps
                         // have dimensions of keys and pages, and boxes of 8 keys
     int cost_sel;       // selected blocks: places of a unit on the line
+    bool whole_sel;     // and whether the last round's units stay whole
     float* part_o;      // [pieces][NQ * 128][D]
     float2* part_ml;    // [pieces][NQ * 128] (m, l)
     int4* desc;         // [grid] unit left open by CTA c: (token, ntok, g, last CTA) or last = -1
@@ -345,7 +346,7 @@ struct WalkSel {
     __device__ __forceinline__ void start(const Params& P, int cta, int grid) {
         const long long units = (long long)P.a.T * P.a.hkv;
         unit = cta;
-        rounds_end = units - units % grid;
+        rounds_end = P.whole_sel ? units : units - units % grid;
         total = (units - rounds_end) * P.cost_sel;
         pieces = min((long long)grid, total);
         x = cta < pieces ? quotient(cta * total, pieces) : 0;

@@ -19,11 +19,11 @@
 // tiles and the epilogue of a unit run under the other products.
 //
 // What bounds it: memory, or what lies before it.  64 requests of one token (4 query heads per
-// KV head, 512 to 32768 keys, 4.36 GB of K and V): 637 us, 6.8 TB/s.  One request of 8192 keys:
+// KV head, 512 to 32768 keys, 4.36 GB of K and V): 635 us, 6.9 TB/s.  One request of 8192 keys:
 // 18 us, of which the data need 5; the rest is the scheduler's first piece and the
-// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 68 us,
-// 4.0 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 322 us, 6.6 TB/s, near the 28 bytes a cycle
-// and SM at which the TMA unit takes boxes of 64 rows.
+// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 63 us,
+// 4.3 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 297 us, 7.2 TB/s, 28 bytes a cycle and SM,
+// near what the TMA unit takes in.
 //
 //   warps 0-7    softmax and epilogue: a warpgroup per stream, one thread per key of the tile
 //                (per value column in the epilogue)

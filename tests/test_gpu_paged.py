@@ -212,7 +212,7 @@ def test_select_many_tokens():
     run(make_case([300, 211], [2000, 211], 16, 4, 128, 64, seed=15, topk=8, pad=3))
 
 
-@pytest.mark.parametrize("hq, hkv, topk", [(8, 4, 2), (64, 2, 1), (80, 2, 3), (16, 8, 16)])
+@pytest.mark.parametrize("hq, hkv, topk", [(8, 4, 2), (64, 2, 1), (80, 2, 3), (16, 8, 16), (8, 1, 64)])
 def test_select_many_units(hq, hkv, topk):
     rng = np.random.default_rng(hq)
     kv = rng.integers(1, 700, 160)
