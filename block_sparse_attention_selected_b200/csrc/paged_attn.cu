@@ -517,8 +517,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
 // Joins the partial results of the unit that CTA blockIdx.x left open, in the order of the
 // pieces.  One warp per row: lane i weighs piece i of each batch of 32, then all lanes add
-// the pieces' columns, eight pieces' loads in flight.
-template <int F16, int D>
+// the pieces' columns, kBatch pieces' loads in flight: eight for units of one tile of rows,
+// which many CTAs share (one token, 8192 keys: 18.4 us; four: 19.4), four for two tiles of rows,
+// mostly cut once (a chunk of 512 behind 3584: 64 us a call; two: 65, eight: 71).
+template <int F16, int D, int kBatch>
 __global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_per_piece) {
     release_dependents();
     depend();
@@ -553,13 +555,13 @@ __global__ void __launch_bounds__(256) k_paged_merge(const Params P, int rows_pe
                 }
             }
             const int n = min(32, np - b);
-            for (int c = 0; c < n; c += 8) {
-                Vec o[8];
+            for (int c = 0; c < n; c += kBatch) {
+                Vec o[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < kBatch; ++i)
                     o[i] = *reinterpret_cast<const Vec*>(P.part_o + at(b + min(c + i, n - 1), row) * D + lane * kV);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     const float wi = __shfl_sync(0xffffffffu, w, (c + i) & 31);
                     if (c + i < n) {
                         const float* e = reinterpret_cast<const float*>(&o[i]);
@@ -602,9 +604,10 @@ cudaError_t launch(const Params& P, int grid, const CUtensorMap& qmap, const CUt
     return launch_dependent(k_paged_attn<F16, D, NQ, SEL>, grid, kPaThreads, smem, stream, P, qmap, kmap, vmap);
 }
 
+template <int kBatch>
 cudaError_t merge(const Params& P, int f16, int grid, int rows_per_piece, cudaStream_t stream) {
-    auto* kernel = P.a.d == 64 ? (f16 ? k_paged_merge<1, 64> : k_paged_merge<0, 64>)
-                               : (f16 ? k_paged_merge<1, 128> : k_paged_merge<0, 128>);
+    auto* kernel = P.a.d == 64 ? (f16 ? k_paged_merge<1, 64, kBatch> : k_paged_merge<0, 64, kBatch>)
+                               : (f16 ? k_paged_merge<1, 128, kBatch> : k_paged_merge<0, 128, kBatch>);
     const dim3 blocks((unsigned)grid, (unsigned)std::min(rows_per_piece / 32, (P.a.G * P.tpu + 7) / 8));
     return launch_dependent(kernel, blocks, 256, 0, stream, P, rows_per_piece);
 }
@@ -703,7 +706,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
                 : dispatch<0, 128>(P, two, grid, qmap, kmap, vmap, stream);
     if (e != cudaSuccess) return e;
     if (P.whole_sel) return cudaSuccess;      // nothing is cut
-    return merge(P, f16, grid, two ? 256 : 128, stream);
+    return two ? merge<4>(P, f16, grid, 256, stream) : merge<8>(P, f16, grid, 128, stream);
 }
 
 }  // namespace nsa
