@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 const Piece& k = S.ring[at_s % kRing];
                 more_s = k.more != 0;
                 const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_s || nt == 0) continue;
+                if (!more_s) break;
                 qb = NQ == 2 ? 0 : units_s & 1;
                 ++units_s;
                 js = first_tile(p0, count_s);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 const Piece& k = S.ring[at_o % kRing];
                 more_o = k.more != 0;
                 const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_o || nt == 0) continue;
+                if (!more_o) break;
                 jo = first_tile(p0, count_o);
                 jo_end = p0 + nt;
                 base_o = count_o - p0;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const float c = p.scale_log2;
         int items = 0;                    // this stream's items so far
         int tiles = 0;                    // NQ = 1: key tiles so far, both streams
-        int units = 0;                    // units with a key tile
+        int units = 0;
         int o_cnt[2] = {0, 0};            // sums each stream has completed
         bool ok = true;
         for (int at = 0;; ++at) {
@@ -420,25 +420,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             const int n0 = NQ == 2 ? nt : (nt + 1 - (tiles & 1)) >> 1, n1 = NQ == 2 ? nt : nt - n0;
             tiles += nt;
             float w0 = 0.f, w1 = 0.f;         // weights of the streams' sums
-            if (nt > 0) {
-                if (NQ == 2) {
-                    if (!(ok = wait(&S.o_full[st], o_cnt[st]++ & 1))) break;
-                } else {
-                    S.xch[units & 1][st][row] = make_float2(m, l);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&S.xbar);
-                    ok = wait(&S.xbar, units & 1);
-                    if (ok && n0 > 0) ok = wait(&S.o_full[0], o_cnt[0]++ & 1);
-                    if (ok && n1 > 0) ok = wait(&S.o_full[1], o_cnt[1]++ & 1);
-                    if (!ok) break;
-                    const float2 a = S.xch[units & 1][0][row], b = S.xch[units & 1][1][row];
-                    m = fmaxf(a.x, b.x);
-                    w0 = a.y != 0.f ? ex2_approx(a.x - m) : 0.f;   // (a NaN sum stays one)
-                    w1 = b.y != 0.f ? ex2_approx(b.x - m) : 0.f;
-                    l = w0 * a.y + w1 * b.y;
-                }
-                tc_fence_after();
+            if (NQ == 2) {
+                if (!(ok = wait(&S.o_full[st], o_cnt[st]++ & 1))) break;
+            } else {
+                S.xch[units & 1][st][row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.xbar);
+                ok = wait(&S.xbar, units & 1);
+                if (ok && n0 > 0) ok = wait(&S.o_full[0], o_cnt[0]++ & 1);
+                if (ok && n1 > 0) ok = wait(&S.o_full[1], o_cnt[1]++ & 1);
+                if (!ok) break;
+                const float2 a = S.xch[units & 1][0][row], b = S.xch[units & 1][1][row];
+                m = fmaxf(a.x, b.x);
+                w0 = a.y != 0.f ? ex2_approx(a.x - m) : 0.f;   // (a NaN sum stays one)
+                w1 = b.y != 0.f ? ex2_approx(b.x - m) : 0.f;
+                l = w0 * a.y + w1 * b.y;
             }
+            tc_fence_after();
             const int tok = k.tok0 + ti, hq = k.g * p.G + head;
             const int slot = k.slot;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
@@ -489,19 +487,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                             l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
-            if (nt > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (NQ == 2) {
-                        mbar_arrive(&S.o_empty[st]);
-                    } else {
-                        if (n0 > 0) mbar_arrive(&S.o_empty[0]);
-                        if (n1 > 0) mbar_arrive(&S.o_empty[1]);
-                    }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (NQ == 2) {
+                    mbar_arrive(&S.o_empty[st]);
+                } else {
+                    if (n0 > 0) mbar_arrive(&S.o_empty[0]);
+                    if (n1 > 0) mbar_arrive(&S.o_empty[1]);
                 }
-                ++units;
             }
+            ++units;
             release(at);
         }
     }

@@ -165,7 +165,7 @@ __device__ __forceinline__ int owner_of(long long x, long long total, long long 
 }
 
 // A unit's piece [u0, u1) of its nt + kUnitCost places (the last ones hold no key tile) as
-// key tiles.  False if it holds none and nothing is to be written for it.
+// key tiles.  False if it holds none, but for a unit without a key tile (nt = 0): write_empty().
 __device__ __forceinline__ bool piece_tiles(long long u0, long long u1, int cta, Piece& k) {
     k.p0 = (int)min(u0, (long long)k.nt);
     k.p1 = (int)min(u1, (long long)k.nt);
@@ -498,7 +498,20 @@ __device__ __forceinline__ void release_piece(Smem& S, int lane, int i) {
     if (lane == 0) mbar_arrive(&S.ring_empty[i % kRing]);
 }
 
-// The scheduler warp: walks the CTA's pieces of work ahead of the others.
+// A unit that sees no key: out = 0, lse = -inf, by one warp.
+__device__ __forceinline__ void write_empty(const PagedAttnArgs& p, const Piece& k, int lane) {
+    for (int t = k.tok0; t < k.tok0 + k.ntok; ++t) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)t * p.hq + k.g * p.G) * p.d);
+        for (int i = lane; i < p.G * p.d / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int h = lane; h < p.G; h += 32) p.lse[(size_t)(k.g * p.G + h) * p.T + t] = -CUDART_INF_F;
+    }
+}
+
+// The scheduler warp: walks the CTA's pieces of work ahead of the others.  Every piece in the
+// ring has a key tile: units that see no key are written here.  (An issuer looks ahead for its
+// next S but gives a place of the ring back with its P V, so that a run of pieces without a
+// tile could fill the ring before it finds one, and nobody could go on.)
 template <bool SEL, class Smem>
 __device__ __forceinline__ void schedule(Smem& S, const Params& P, const Waiter& wait, int tpu, int cta, int grid,
                                          int lane) {
@@ -520,10 +533,11 @@ __device__ __forceinline__ void schedule(Smem& S, const Params& P, const Waiter&
         const int at = i % kRing;
         if (!wait(&S.ring_empty[at], ((i / kRing) & 1) ^ 1)) break;
         Piece k{};
-        if (SEL) {
-            if (!wsel.next(P, cta, grid, lane, S.list[at], k)) k.more = 0;
-        } else {
-            if (!wall.next(P, tpu, cta, k)) k.more = 0;
+        for (bool more = true; more;) {
+            more = SEL ? wsel.next(P, cta, grid, lane, S.list[at], k) : wall.next(P, tpu, cta, k);
+            if (!more) k.more = 0;
+            else if (k.nt == 0) write_empty(p, k, lane);
+            else break;
         }
         if (k.more && k.slot == 2 * cta + 1)     // its last key tile's place on the line
             open = make_int4(k.tok0, k.ntok, k.g,
@@ -559,7 +573,7 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
     bool nx_live = false;
     int nx_page = 0, nx_row = 0, nx_g = 0;
     auto advance = [&]() -> bool {
-        while (more && j == j_end) {          // the next piece with a key tile
+        if (j == j_end) {                     // the next piece
             if (at >= 0) release_piece(S, lane, at);
             if (!fetch_piece(S, wait, ++at)) return false;
             const Piece& k = S.ring[at % kRing];

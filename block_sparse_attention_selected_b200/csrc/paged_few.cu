@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const Piece& k = S.ring[at_s % kRing];
                 more_s = k.more != 0;
                 const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_s || nt == 0) continue;
+                if (!more_s) break;
                 qb = units_s & 1;
                 ++units_s;
                 js = first_tile(p0, count_s);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const Piece& k = S.ring[at_o % kRing];
                 more_o = k.more != 0;
                 const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_o || nt == 0) continue;
+                if (!more_o) break;
                 jo = first_tile(p0, count_o);
                 jo_end = p0 + nt;
                 base_o = count_o - p0;
@@ -332,18 +332,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         };
         // A finished unit's output.  It waits for the unit's last P V and for the other stream,
         // so it is left until the first tile of the next unit is on its way.
-        struct Done { int at, par, phase, nt, n0, n1, c0, c1; };
-        Done done{-1, 0, 0, 0, 0, 0, 0, 0};
+        struct Done { int at, par, n0, n1, c0, c1; };     // par: the unit's parity
+        Done done{-1, 0, 0, 0, 0, 0};
         auto finish = [&]() -> bool {
             const Piece& k = S.ring[done.at % kRing];
-            const int par = done.par, nt = done.nt, rows = k.ntok * p.G;
-            if (nt > 0) {
-                bool fine = wait(&S.xbar, done.phase);
-                if (fine && done.n0 > 0) fine = wait(&S.o_full[0][done.c0 & 1], (done.c0 >> 1) & 1);
-                if (fine && done.n1 > 0) fine = wait(&S.o_full[1][done.c1 & 1], (done.c1 >> 1) & 1);
-                if (!fine) return false;
-                tc_fence_after();
-            }
+            const int par = done.par, rows = k.ntok * p.G;
+            bool fine = wait(&S.xbar, par);
+            if (fine && done.n0 > 0) fine = wait(&S.o_full[0][done.c0 & 1], (done.c0 >> 1) & 1);
+            if (fine && done.n1 > 0) fine = wait(&S.o_full[1][done.c1 & 1], (done.c1 >> 1) & 1);
+            if (!fine) return false;
+            tc_fence_after();
             // this thread: value column `key` of half of the rows (the other half: the other
             // warpgroup)
             const int slot = k.slot, tok0 = k.tok0, hq0 = k.g * p.G;
@@ -357,16 +355,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 for (int y = 0; y < 8; ++y) {
                     const int r = x + y;
                     if (r >= rows) break;
-                    float mm = -CUDART_INF_F, ll = 0.f, w0 = 0.f, w1 = 0.f;
-                    if (nt > 0) {
-                        const float m0 = S.m[par][0][r], m1 = S.m[par][1][r];
-                        const float l0 = S.l[par][0][0][r] + S.l[par][0][1][r] + S.l[par][0][2][r] + S.l[par][0][3][r];
-                        const float l1 = S.l[par][1][0][r] + S.l[par][1][1][r] + S.l[par][1][2][r] + S.l[par][1][3][r];
-                        mm = fmaxf(m0, m1);
-                        w0 = l0 != 0.f ? ex2_approx(m0 - mm) : 0.f;   // (a NaN sum stays one)
-                        w1 = l1 != 0.f ? ex2_approx(m1 - mm) : 0.f;
-                        ll = w0 * l0 + w1 * l1;
-                    }
+                    const float m0 = S.m[par][0][r], m1 = S.m[par][1][r];
+                    const float l0 = S.l[par][0][0][r] + S.l[par][0][1][r] + S.l[par][0][2][r] + S.l[par][0][3][r];
+                    const float l1 = S.l[par][1][0][r] + S.l[par][1][1][r] + S.l[par][1][2][r] + S.l[par][1][3][r];
+                    const float mm = fmaxf(m0, m1);
+                    const float w0 = l0 != 0.f ? ex2_approx(m0 - mm) : 0.f;   // (a NaN sum stays one)
+                    const float w1 = l1 != 0.f ? ex2_approx(m1 - mm) : 0.f;
+                    const float ll = w0 * l0 + w1 * l1;
                     // a weight of 0 belongs to a sum that may never have been started
                     const float o = (w0 != 0.f ? w0 * a[y] : 0.f) + (w1 != 0.f ? w1 * b[y] : 0.f);
                     if (slot < 0) {
@@ -382,13 +377,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 }
             }
-            if (nt > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (done.n0 > 0) mbar_arrive(&S.o_empty[0][done.c0 & 1]);
-                    if (done.n1 > 0) mbar_arrive(&S.o_empty[1][done.c1 & 1]);
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (done.n0 > 0) mbar_arrive(&S.o_empty[0][done.c0 & 1]);
+                if (done.n1 > 0) mbar_arrive(&S.o_empty[1][done.c1 & 1]);
             }
             release_piece(S, lane, done.at);
             done.at = -1;
@@ -491,21 +484,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             if (!ok) break;
             if (done.at >= 0 && !(ok = finish())) break;     // (no tile of this unit for the stream)
-            done = {at, units & 1, units & 1, nt, n0, n1, o_next[0], o_next[1]};
-            if (nt > 0) {
-                // the rows' references and sums, for both streams' threads
-                if (quad == 0 && lane == 0) {
+            done = {at, units & 1, n0, n1, o_next[0], o_next[1]};
+            // the rows' references and sums, for both streams' threads
+            if (quad == 0 && lane == 0) {
 #pragma unroll
-                    for (int r = 0; r < N; ++r) S.m[done.par][st][r] = m[r];
-                }
-                const float lsum = transpose_reduce(l, lane, [](float a, float b) { return a + b; });
-                if (lane < N) S.l[done.par][st][quad][lane] = lsum;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.xbar);
-                o_next[0] += n0 > 0;
-                o_next[1] += n1 > 0;
-                ++units;
+                for (int r = 0; r < N; ++r) S.m[done.par][st][r] = m[r];
             }
+            const float lsum = transpose_reduce(l, lane, [](float a, float b) { return a + b; });
+            if (lane < N) S.l[done.par][st][quad][lane] = lsum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.xbar);
+            o_next[0] += n0 > 0;
+            o_next[1] += n1 > 0;
+            ++units;
         }
         if (ok && done.at >= 0) finish();
     }
