@@ -170,11 +170,26 @@ def _ws_key(dev: torch.device):
     return (dev, torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _capturing(dev: torch.device) -> bool:
+    """Whether the device's current stream is being captured into a CUDA graph."""
+    if not torch.cuda.is_initialized():
+        return False
+    with torch.cuda.device(dev):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def get_workspace(nbytes: int, device) -> torch.Tensor:
     """A cached uint8 device buffer of at least nbytes (grown on demand) for the
     device's current stream; it is allocated on that stream, so the caching allocator
-    orders its reuse after the calls that used it."""
+    orders its reuse after the calls that used it.
+
+    While that stream is being captured into a CUDA graph the buffer is a new one of the
+    graph's own memory and is not cached: a cached buffer would be shared with other graphs
+    and with eager calls, which may overlap with a replay, and could be freed under the
+    graph.  (nsa_sel_check_status of a replay then needs the call's `workspace`.)"""
     dev = torch.device(device)
+    if _capturing(dev):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     key = _ws_key(dev)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:

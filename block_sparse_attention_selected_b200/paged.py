@@ -218,17 +218,11 @@ def nsa_sel_paged_attn_workspace_size(total_tokens, num_seqs, hq, hkv, head_dim)
 _workspace_bytes: dict = {}   # head_dim -> bytes: the size depends on nothing else
 
 
-def _paged_workspace(T, R, hq, hkv, d, q, stream):
+def _paged_workspace(T, R, hq, hkv, d, q):
     nbytes = _workspace_bytes.get(d)
     if nbytes is None:
         nbytes = _workspace_bytes[d] = nsa_sel_paged_attn_workspace_size(T, R, hq, hkv, d)
-    # A call that is being captured takes its workspace from the graph's own memory: the
-    # cached one would be shared with other graphs and with eager calls, which may overlap
-    # with a replay.
-    if _capturing():
-        return q.new_empty(nbytes, dtype=torch.uint8)
-    ws = _ws_cache.get((q.device, stream))
-    return ws if ws is not None and ws.numel() >= nbytes else get_workspace(nbytes, q.device)
+    return get_workspace(nbytes, q.device)
 
 
 def _attend_plain(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, block_idx, block_size, scale,
@@ -241,6 +235,7 @@ def _attend_plain(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, blo
     stream = _raw_stream(device)
     ws = workspace
     if ws is None:
+        # (being captured: not from the cache, see get_workspace)
         ws = None if _capturing() else _ws_cache.get((q.device, stream))
         if ws is None:
             return None
@@ -285,7 +280,7 @@ def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection
         ws = workspace
         _packed(ws, "workspace", torch.uint8, 1, index)
     else:
-        ws = _paged_workspace(T, R, hq, cshape[2], d, q, stream)
+        ws = _paged_workspace(T, R, hq, cshape[2], d, q)
     _call(fn, index, q.data_ptr(), qs[0], qs[1], T, hq, ctypes.byref(cache), cu, kv, R, *table, *selection,
           d ** -0.5 if scale is None else float(scale), int(window_size), to, lse_to, ws.data_ptr(), ws.numel(),
           stream, flag)

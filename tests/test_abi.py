@@ -307,3 +307,25 @@ def test_noalloc_size_boundary(lib):
                                                       fake, None)
     assert call(lo + 1) == 3                             # NSA_ERR_WORKSPACE
     assert call(lo) != 3                                 # past the size check
+
+
+def test_workspace_of_a_captured_call_is_not_cached(monkeypatch):
+    """While a stream is being captured every call gets a buffer of its own, and the cache
+    is neither read nor written."""
+    import types
+    import torch
+    state = {"capturing": False}
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda dev=None: types.SimpleNamespace(cuda_stream=11))
+    monkeypatch.setattr(nsa, "_capturing", lambda dev: state["capturing"])
+    real_empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda n, dtype=None, device=None: real_empty(n, dtype=dtype))
+    nsa.release_workspaces()
+    dev = torch.device("cuda", 0)
+    eager = nsa.get_workspace(100, dev)
+    state["capturing"] = True
+    a, b = nsa.get_workspace(100, dev), nsa.get_workspace(1000, dev)
+    assert a is not eager and b is not a and b is not eager
+    state["capturing"] = False
+    assert nsa.get_workspace(100, dev) is eager and list(nsa._ws_cache.values()) == [eager]
+    nsa.release_workspaces()
