@@ -158,6 +158,11 @@ nsa_status_t check_device(int* num_sms, nsa_stream_t stream_) {
     return NSA_OK;
 }
 
+// One lock per workspace, near enough: two that share a slot wait for each other's launches.
+static std::mutex g_launch_locks[61];
+LaunchLock::LaunchLock(const void* workspace)
+    : lock_(g_launch_locks[(reinterpret_cast<uintptr_t>(workspace) >> 8) % 61]) {}
+
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -398,6 +403,7 @@ nsa_status_t fwd_impl(const void* q, const void* k, const void* v, const int32_t
     int num_sms = 0;
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     const Layout L = make_layout(D, false);
     Carved c = carve(D, L, workspace, cu_seqlens, block_idx, swin);
     const PhaseMarks pm{events, num_events, stream, launches};
@@ -512,6 +518,7 @@ nsa_status_t bwd_impl(const void* q, const void* k, const void* v, const void* o
     int num_sms = 0;
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     const Layout L = make_layout(D, true);
     Carved c = carve(D, L, workspace, cu_seqlens, block_idx, swin);
     const PhaseMarks pm{events, num_events, stream, launches};
@@ -696,6 +703,7 @@ nsa_status_t nsa_sel_invert_index(const int32_t* cu_seqlens, int num_seqs, int t
     int num_sms = 0;
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     const Layout L = make_layout(D, false);
     Carved c = carve(D, L, workspace, cu_seqlens, block_idx);
     if (cudaMemsetAsync(c.st, 0, sizeof(DevStatus), stream) != cudaSuccess) return NSA_ERR_CUDA;
@@ -735,6 +743,7 @@ nsa_status_t nsa_sel_validate_indices(const int32_t* cu_seqlens, int num_seqs, i
     nsa_status_t s;
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     DevStatus* st = static_cast<DevStatus*>(workspace);
     if (cudaMemsetAsync(st, 0, sizeof(DevStatus), stream) != cudaSuccess) return NSA_ERR_CUDA;
     if ((s = cuda_status(launch_validate(cu_seqlens, num_seqs, total_tokens, hkv, block_idx, topk,
@@ -801,6 +810,7 @@ nsa_status_t nsa_sel_block_scores(const void* q, const void* k_cmp, int k_cmp_ro
     nsa_status_t s = check_device(&num_sms, stream_);
     if (s != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     DevStatus* st = static_cast<DevStatus*>(workspace);
     int32_t* tile_off = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
                                                    align256(sizeof(DevStatus)));
@@ -838,6 +848,7 @@ nsa_status_t nsa_sel_bsfa_fwd(const void* q, const void* k, const void* v, const
     nsa_status_t s = check_device(&num_sms, stream_);
     if (s != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     DevStatus* st = static_cast<DevStatus*>(workspace);
     int32_t* tile_off = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
                                                    align256(sizeof(DevStatus)));
@@ -872,6 +883,7 @@ nsa_status_t nsa_sel_select_topk(const float* scores, const int32_t* cu_seqlens,
     nsa_status_t s = check_device(&num_sms, stream_);
     if (s != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(workspace);
     DevStatus* st = static_cast<DevStatus*>(workspace);
     if (cudaMemsetAsync(st, 0, sizeof(DevStatus), stream) != cudaSuccess) return NSA_ERR_CUDA;
     return cuda_status(launch_select_topk(scores, cu_seqlens, num_seqs, total_tokens, hkv, nb_stride,
@@ -1010,6 +1022,7 @@ nsa_status_t nsa_sel_invert_index_noalloc(const int32_t* cu_seqlens, int num_seq
     void* scratch = nullptr;
     if ((s = scratch_for_current_device(&scratch)) != NSA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const LaunchLock lock(scratch);
     Carved c = carve(D, L, scratch, cu_seqlens, block_idx);
     if (cudaMemsetAsync(c.st, 0, sizeof(DevStatus), stream) != cudaSuccess) return NSA_ERR_CUDA;
     if (total_tokens == 0) {

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <utility>
 
 #include "../../include/nsa_sel.h"
@@ -42,6 +43,16 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_
 // Host helpers of the C ABI (api.cu).
 nsa_status_t check_device(int* num_sms, nsa_stream_t stream);
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn();   // null if the driver lacks it
+// The kernels of one call hand their results over through its workspace.  Threads that share a
+// stream and a workspace (the binding keeps one per stream) therefore launch whole calls, one
+// after the other: held from a call's first launch to its last.
+class LaunchLock {
+public:
+    explicit LaunchLock(const void* workspace);
+
+private:
+    std::lock_guard<std::mutex> lock_;
+};
 
 // The paged-attention kernels report one status byte per CTA, in the unused end of the status
 // block (every other call clears the whole block first).

@@ -49,6 +49,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
         return NSA_ERR_WORKSPACE;
     int num_sms = 0;
     if ((s = check_device(&num_sms, stream_)) != NSA_OK) return s;
+    const LaunchLock lock(ws);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     DevStatus* st = static_cast<DevStatus*>(ws);
     if (T == 0)
