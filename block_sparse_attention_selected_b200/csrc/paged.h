@@ -115,6 +115,7 @@ struct PagedAttnArgs {
     uint16_t* out;           // [T, hq, d]
     float* lse;              // [hq, T] or null
     DevStatus* st;
+    bool test_skip;          // NSA_TEST_SKIP_ARRIVE: the first K tile of CTA 0 never counts as there
 };
 size_t paged_attn_workspace(int d);   // bytes, the status block included
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, int f16, int num_sms, cudaStream_t stream);

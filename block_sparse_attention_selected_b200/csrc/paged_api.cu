@@ -32,7 +32,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
                        size_t ws_bytes, nsa_stream_t stream_, unsigned flags) {
     nsa_status_t s = check_cache(c);
     if (s != NSA_OK) return s;
-    if ((flags & ~NSA_F16) != 0) return NSA_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)(NSA_F16 | NSA_TEST_SKIP_ARRIVE)) return NSA_ERR_INVALID_ARG;
     if (T < 0 || hq < 1 || R < 1 || width < 1 || table_stride < width || hq % c->hkv != 0)
         return NSA_ERR_INVALID_ARG;
     if (nsa_sel_paged_attn_workspace_size(T, R, hq, c->hkv, c->head_dim) == 0)
@@ -85,6 +85,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     p.st = st;
+    p.test_skip = (flags & NSA_TEST_SKIP_ARRIVE) != 0;
     return launch_paged_attn(p, (flags & NSA_F16) ? 1 : 0, num_sms, stream) == cudaSuccess ? NSA_OK
                                                                                            : NSA_ERR_CUDA;
 }

@@ -63,6 +63,7 @@ struct alignas(1024) PaSmem {
     uint64_t xbar, drain;
     uint32_t tmem_base;
     int abort_flag, err;
+    int loaded[3];                            // K tiles, V tiles and Qs that the producer asked for
 };
 
 template <int N>
@@ -102,7 +103,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             mbar_init(&S.o_empty[i], NQ == 2 ? 4 : 8);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&S.kv_full[i], 1);
+            // (a test: the first tile of K, place 0, waits for an arrival that never comes)
+            mbar_init(&S.kv_full[i], i == 0 && cta == 0 && p.test_skip ? 2 : 1);
             mbar_init(&S.kv_empty[i], NQ);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -507,7 +509,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == 8) {
+        if (S.abort_flag) land_copies<NQ, Stages>(S, lane);
+        tmem_dealloc(tmem, 512);
+    }
     if (tid == 0) finish_status(p.st, S.err, cta, grid);
 }
 

@@ -440,31 +440,34 @@ template <int kRings, int kPer, int kAhead>
 struct Ring {
     static constexpr int kRun = kRings * kAhead;     // K tiles loaded ahead of V, over all rings
     struct At { int stage; uint32_t phase; };
+    __device__ __forceinline__ static uint32_t phase(int place) { return (uint32_t)(place / kPer) & 1u; }
     __device__ __forceinline__ static At at(int t, int place) {
-        return {(kRings == 2 ? (t & 1) * kPer : 0) + place % kPer, (uint32_t)(place / kPer) & 1u};
+        return {(kRings == 2 ? (t & 1) * kPer : 0) + place % kPer, phase(place)};
     }
-    __device__ __forceinline__ static At k(int t) {
+    __device__ __forceinline__ static int k_place(int t) {
         const int i = kRings == 2 ? t >> 1 : t;
-        return at(t, i < kAhead ? i : 2 * i - kAhead + 1);
+        return i < kAhead ? i : 2 * i - kAhead + 1;
     }
-    __device__ __forceinline__ static At v(int t) {
-        const int i = kRings == 2 ? t >> 1 : t;
-        return at(t, 2 * i + kAhead);
-    }
+    __device__ __forceinline__ static int v_place(int t) { return 2 * (kRings == 2 ? t >> 1 : t) + kAhead; }
+    __device__ __forceinline__ static At k(int t) { return at(t, k_place(t)); }
+    __device__ __forceinline__ static At v(int t) { return at(t, v_place(t)); }
 };
 
-// Bounded wait of a whole warp; false in every lane if any lane gave up, or once a warp of
-// the CTA has.
+// Bounded wait of a whole warp; false in every lane if any lane gave up.  A role that finds
+// nothing to wait for goes on whether or not another has given up; one that has to wait then gives
+// up too.  (Looking at the flag before every wait, and in the loop: selected blocks of a chunk of
+// 512 tokens 304 us, in the loop alone 288; 64 bits of the clock: 291.)
+static_assert(kWaitBudgetCycles < (1ll << 32), "the waits count cycles in 32 bits");
 struct Waiter {
     volatile int* abort_flag;
     int* err;
     __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) const {
-        if (*abort_flag) return false;
         if (mbar_try_wait(bar, parity)) return true;
-        const long long start = clock64();
+        const uint32_t start = (uint32_t)clock();
 #pragma unroll 1
         while (!mbar_try_wait(bar, parity)) {
-            if (clock64() - start > kWaitBudgetCycles) {
+            if (*abort_flag) return false;
+            if ((uint32_t)clock() - start > (uint32_t)kWaitBudgetCycles) {
                 *err = NSA_ERR_TIMEOUT;
                 *abort_flag = 1;
                 return false;
@@ -666,21 +669,38 @@ __device__ __forceinline__ void produce(Smem& S, const Params& P, const Waiter& 
         }
         --pending;
     }
-    if (*wait.abort_flag && lane == 0) {   // let copies still in flight land before the CTA exits
-        const long long start = clock64();
-        auto land = [&](uint64_t* bar, uint32_t parity) {
-            while (!mbar_try_wait(bar, parity) && clock64() - start < kWaitBudgetCycles) {}
-        };
-        for (int i = 0; i < 2; ++i) {
-            const int uses = kTiles == 2 ? (i == 0 ? units : 0) : (units + 1 - i) / 2;
-            if (uses > 0) land(&S.q_full[i], (uses - 1) & 1);
-        }
-        // the tiles that may lie in the stages now, the oldest first
-        for (int t = max(tk - 2 * Smem::kStages, 0); t < tk; ++t) {
-            land(&S.kv_full[Stages::k(t).stage], Stages::k(t).phase);
-            if (t < tv) land(&S.kv_full[Stages::v(t).stage], Stages::v(t).phase);
-        }
+    if (lane == 0) {
+        S.loaded[0] = tk;
+        S.loaded[1] = tv;
+        S.loaded[2] = units;
     }
+    __syncwarp();
+}
+
+// Where a role gave up, copies may be in flight that nobody waits for: they land before the CTA
+// exits.  By the producer warp, when every role has ended; a lane per stage, for its last copy.
+template <int kTiles, class Stages, class Smem>
+__device__ __forceinline__ void land_copies(Smem& S, int lane) {
+    const int tk = S.loaded[0], tv = S.loaded[1], units = S.loaded[2];
+    int place = -1;
+    for (int t = max(tk - 2 * Smem::kStages, 0); t < tk; ++t) {
+        const int k = Stages::k_place(t), v = t < tv ? Stages::v_place(t) : -1;
+        if (Stages::at(t, k).stage == lane) place = max(place, k);
+        if (v >= 0 && Stages::at(t, v).stage == lane) place = max(place, v);
+    }
+    uint64_t* bar = nullptr;
+    uint32_t parity = 0;
+    if (lane < Smem::kStages) {
+        if (place >= 0) bar = &S.kv_full[lane];
+        parity = Stages::phase(place);
+    } else if (lane < Smem::kStages + 2) {
+        const int i = lane - Smem::kStages;
+        const int uses = kTiles == 2 ? (i == 0 ? units : 0) : (units + 1 - i) / 2;
+        if (uses > 0) bar = &S.q_full[i];
+        parity = (uint32_t)(uses - 1) & 1u;
+    }
+    const uint32_t start = (uint32_t)clock();
+    while (bar && !mbar_try_wait(bar, parity) && (uint32_t)clock() - start < (uint32_t)(kWaitBudgetCycles / 64)) {}
     __syncwarp();
 }
 

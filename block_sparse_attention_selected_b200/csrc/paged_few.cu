@@ -64,6 +64,7 @@ struct alignas(1024) FewSmem {
     uint64_t xbar, drain;
     uint32_t tmem_base;
     int abort_flag, err;
+    int loaded[3];                            // K tiles, V tiles and Qs that the producer asked for
 };
 
 // 8 and 16 fp32 columns of this thread's TMEM lane
@@ -125,7 +126,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mbar_init(&S.meet[i], 4);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&S.kv_full[i], 1);
+            // (a test: the first tile of K, place 0, waits for an arrival that never comes)
+            mbar_init(&S.kv_full[i], i == 0 && cta == 0 && p.test_skip ? 2 : 1);
             mbar_init(&S.kv_empty[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -506,7 +508,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, kCols);
+    if (warp == 8) {
+        if (S.abort_flag) land_copies<1, Stages>(S, lane);
+        tmem_dealloc(tmem, kCols);
+    }
     if (tid == 0) finish_status(p.st, S.err, cta, grid);
 }
 

@@ -136,7 +136,8 @@ NSA_API nsa_status_t nsa_sel_attn_bwd_profiled(
 /* Option flags of the _ex calls below (OR-ed). */
 #define NSA_BWD_REUSE_INDEX 1u
 #define NSA_F16 2u
-/* Test-only options of nsa_sel_attn_fwd_ex, for the failure-detection tests (no
+/* Test-only options of nsa_sel_attn_fwd_ex (and NSA_TEST_SKIP_ARRIVE of the paged
+ * attention calls, see there), for the failure-detection tests (no
  * counterpart in the pages).  NSA_TEST_SHORT_WAITS limits every bounded wait of the
  * call's kernels to 0x01010101 SM cycles (about 8.6 ms at 1.965 GHz) instead of about
  * one second.  NSA_TEST_SKIP_ARRIVE makes one Q loader warp of the first CTA of the
@@ -415,7 +416,11 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  * Cache rows that hold no visible key may hold anything, infinities and NaN too.  (A
  * non-finite V row that some query of a request sees can also reach the outputs of that
  * request's queries of the same KV head that do not see it: 0 times infinity in a shared
- * product.)  The scale must be positive and finite.  Other flag bits return NSA_ERR_INVALID_ARG.
+ * product.)  The scale must be positive and finite.
+ * Test-only flag NSA_TEST_SKIP_ARRIVE: an arrival is missing for the first CTA's first tile of K: the
+ * wait for the tile expires after about a second, the CTA lets its copies and tensor-core work end, the call records
+ * NSA_ERR_TIMEOUT with undefined outputs, and the device stays usable.  Other flag bits return
+ * NSA_ERR_INVALID_ARG.
  * Device-side problems (nsa_sel_check_status): cu_seqlens decreasing or beyond
  * total_tokens, kv_lens beyond the table's row, a used table entry outside [0, num_pages):
  * NSA_ERR_BAD_INDEX, the outputs of that request undefined; no access leaves the cache. */
