@@ -213,15 +213,17 @@ struct WalkAll {
         }
         return c;
     }
-    // false: the lengths are not sound
+    // false: the lengths are not sound.  Requests that overlap get no work: the line's sums hold
+    // for total_tokens tokens, not for more.
     __device__ __forceinline__ bool start(const Params& P, int tpu, int cta, int grid, int lane) {
         const PagedAttnArgs& p = P.a;
         const int per = (p.R + 31) / 32;
         long long mine = 0;
-        int count = 0;
+        int count = 0, tokens = 0;
         int most = 0;                       // costs of the most expensive unit
         bool good = true;
         whole = false;
+        x = x1 = u0 = 0;
         auto load = [&](int i, int end) {
             Req q{0, 0, 0};
             if (i < end) q = request(p, i);
@@ -231,6 +233,8 @@ struct WalkAll {
             const int i = lane * per + s;
             const Req q = load(i, p.R);
             if (i < p.R) good &= request_ok(p, i);
+            tokens += __reduce_add_sync(0xffffffffu, q.n);
+            if (tokens > p.T) return false;
             mine += cost(p, q, tpu, lane);
             const int last = (q.n + tpu - 1) / tpu - 1;
             count += last + 1;
@@ -239,20 +243,17 @@ struct WalkAll {
         }
         long long inc = scan(mine, lane);
         long long all = __shfl_sync(0xffffffffu, inc, 31);
-        {
-            // (units of one KV head: at most total_tokens)
-            const long long units = (long long)__reduce_add_sync(0xffffffffu, count) * p.hkv;
-            most = __reduce_max_sync(0xffffffffu, most);
-            whole = quotient(units + grid - 1, grid) * most <= quotient(all * p.hkv + grid - 1, grid) + kMergeCost;
-            if (whole) {
-                mine = count;
-                inc = scan(mine, lane);
-                all = __shfl_sync(0xffffffffu, inc, 31);
-            }
+        // (units of one KV head: at most total_tokens)
+        const long long units = (long long)__reduce_add_sync(0xffffffffu, count) * p.hkv;
+        most = __reduce_max_sync(0xffffffffu, most);
+        whole = quotient(units + grid - 1, grid) * most <= quotient(all * p.hkv + grid - 1, grid) + kMergeCost;
+        if (whole) {
+            mine = count;
+            inc = scan(mine, lane);
+            all = __shfl_sync(0xffffffffu, inc, 31);
         }
         total = all * p.hkv;
         pieces = min((long long)grid, total);
-        x = x1 = u0 = 0;
         head = r = qt = 0;
         good = __all_sync(0xffffffffu, good);
         if (cta >= pieces) return good;

@@ -423,7 +423,8 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  * NSA_ERR_INVALID_ARG.
  * Device-side problems (nsa_sel_check_status): cu_seqlens decreasing or beyond
  * total_tokens, kv_lens beyond the table's row, a used table entry outside [0, num_pages):
- * NSA_ERR_BAD_INDEX, the outputs of that request undefined; no access leaves the cache. */
+ * NSA_ERR_BAD_INDEX, the outputs of that request undefined (of every request, where decreasing
+ * cu_seqlens let requests overlap); no access leaves the cache. */
 NSA_API size_t nsa_sel_paged_attn_workspace_size(int total_tokens, int num_seqs, int hq, int hkv,
                                                  int head_dim);
 NSA_API nsa_status_t nsa_sel_paged_attn_fwd(const void *q, int64_t q_token_stride,

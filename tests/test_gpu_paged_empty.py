@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import block_sparse_attention_selected_b200 as nsa
 from paged_util import make_case
-from test_gpu_paged import run
+from test_gpu_paged import attend, cuda, run, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,28 @@ def test_selected_rows_without_a_block(rows, hq, d):
     got = run(c)
     bare = torch.from_numpy(bare).cuda()
     assert torch.all(got[0][bare] == 0) and torch.all(torch.isneginf(got[1][:, bare]))
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+def test_requests_that_overlap_are_refused(topk):
+    c = make_case([3, 2, 3], [300, 90, 200], 8, 2, 64, 64, seed=6, topk=topk, poison=False)
+    ts = list(tensors(c))
+    ts[3] = cuda(np.array([0, 6, 1, 8], np.int32))
+    attend(c, ts)
+    assert nsa.nsa_sel_check_status() == 6
+    run(c)
+
+
+def test_requests_that_overlap_by_more_than_their_sums_hold():
+    # every other request has all rows: 2^31 units of one token
+    T, R, hq, d = 1 << 18, 16384, 128, 64
+    q = torch.zeros(T * 8 + hq * d, dtype=torch.bfloat16, device="cuda").as_strided((T, hq, d), (8, 8, 1))
+    k, v = (torch.zeros(4, 16, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu = torch.zeros(R + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    kv = torch.full((R,), 64, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").expand(R, 4).contiguous()
+    out = torch.full((T, hq, d), 77.0, dtype=q.dtype, device="cuda")
+    nsa.nsa_sel_paged_attn_fwd(q, k, v, cu, kv, table, out=out, with_lse=False)
+    assert nsa.nsa_sel_check_status() == 6
+    assert bool((out == 77.0).all())
