@@ -106,6 +106,8 @@ nsa_status_t nsa_sel_paged_plan(const int32_t* new_lens, const int32_t* cached_l
     if (!page_size_ok(page_size) || num_seqs > kMaxSeqs || total_tokens >= (1 << 25))
         return NSA_ERR_UNSUPPORTED;
     if ((long long)table_width * page_size >= (1ll << 31)) return NSA_ERR_UNSUPPORTED;
+    // (the kernel counts fresh pages in 32 bits and walks them in steps of its grid's threads)
+    if ((long long)num_seqs * table_width >= (1ll << 31) - (1 << 17)) return NSA_ERR_UNSUPPORTED;
     if (!new_lens || !cached_lens || !block_table || !cu_seqlens || !kv_lens || !pages_used ||
         (num_free > 0 && !free_pages) || (total_tokens > 0 && (!slots || !positions)))
         return NSA_ERR_INVALID_ARG;

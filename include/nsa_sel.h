@@ -362,6 +362,7 @@ typedef struct {
  *   free_pages    int32 [num_free] page numbers in the order they are to be taken
  *   block_table   int32 [num_seqs, table_width], row stride table_stride (elements): the
  *                 entries of fresh pages are written, all others are left as they were
+ *                 (num_seqs * table_width < 2^31 - 2^17)
  *   total_tokens  rows of slots and positions, >= the sum of new_lens (more: a padded
  *                 batch)
  *   cu_seqlens    int32 [num_seqs + 1] (written): exclusive prefix sums of new_lens

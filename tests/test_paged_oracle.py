@@ -172,3 +172,12 @@ def test_attention_flags(lib):
             assert attend(lib, flags=flags, sel=sel) in (4, 7)
         for flags in (1, 4, 0x100, 0x300, 0x400, 1 << 31):
             assert attend(lib, flags=flags, sel=sel) == 1
+
+
+def test_plan_refuses_tables_whose_pages_it_cannot_count(lib):
+    def call(R, width):
+        return lib.nsa_sel_paged_plan(FAKE, FAKE, R, FAKE, 4, FAKE, width, width, 16, 3, FAKE, FAKE, FAKE, FAKE,
+                                      FAKE, None)
+    assert call(8192, 1 << 18) == 2 and call(16384, (1 << 17) - 8) == 2
+    if not torch.cuda.is_available():
+        assert call(16384, (1 << 17) - 9) in (4, 7)
