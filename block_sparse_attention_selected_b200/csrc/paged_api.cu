@@ -9,7 +9,8 @@ namespace {
 constexpr int kMaxSeqs = 16384;   // the request lengths are scanned in shared memory
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool mult8(int64_t x) { return (x & 7) == 0; }
+// A stride over `size` places, of at least `least` elements; over one place it is never used.
+bool stride_ok(int64_t x, int64_t size, int64_t least) { return size <= 1 || (x >= least && (x & 7) == 0); }
 
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
@@ -19,8 +20,8 @@ nsa_status_t check_cache(const nsa_paged_cache_t* c) {
     if (!page_size_ok(c->page_size) || (c->head_dim != 64 && c->head_dim != 128))
         return NSA_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return NSA_ERR_INVALID_ARG;
-    if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 || !mult8(c->page_stride) ||
-        !mult8(c->token_stride) || !mult8(c->head_stride))
+    if (!stride_ok(c->page_stride, c->num_pages, 1) || !stride_ok(c->token_stride, c->page_size, 1) ||
+        !stride_ok(c->head_stride, c->hkv, 1))
         return NSA_ERR_INVALID_ARG;
     return NSA_OK;
 }
@@ -42,7 +43,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu, 4) ||
         !aligned(kv_lens, 4) || !aligned(table, 4) || !aligned(bidx, 4) || !aligned(ws, 256))
         return NSA_ERR_INVALID_ARG;
-    if (q_token_stride < 0 || q_head_stride < 0 || !mult8(q_token_stride) || !mult8(q_head_stride))
+    if (T > 0 && (!stride_ok(q_token_stride, T, 1) || !stride_ok(q_head_stride, hq, 1)))
         return NSA_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !(scale < 1e30f) || swin < 0) return NSA_ERR_INVALID_ARG;
     if (ws_bytes < nsa_sel_paged_attn_workspace_size(T, R, hq, c->hkv, c->head_dim))
@@ -148,8 +149,10 @@ nsa_status_t nsa_sel_paged_write_kv(const void* k, const void* v, int64_t k_toke
     if (total_tokens >= (1 << 25)) return NSA_ERR_UNSUPPORTED;
     if (total_tokens > 0 && (!k || !v || !slots)) return NSA_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return NSA_ERR_INVALID_ARG;
-    for (int64_t x : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
-        if (x < 0 || !mult8(x)) return NSA_ERR_INVALID_ARG;
+    if (total_tokens > 0 &&
+        (!stride_ok(k_token_stride, total_tokens, 0) || !stride_ok(v_token_stride, total_tokens, 0) ||
+         !stride_ok(k_head_stride, cache->hkv, 0) || !stride_ok(v_head_stride, cache->hkv, 0)))
+        return NSA_ERR_INVALID_ARG;
     int num_sms = 0;
     if ((s = check_device(&num_sms, stream)) != NSA_OK) return s;
     if (total_tokens == 0) return NSA_OK;

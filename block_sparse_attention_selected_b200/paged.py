@@ -118,7 +118,7 @@ def _cache_arg(k_cache, v_cache, et, index):
     shape = k_cache.shape
     if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if strides != other:
+    if any(a != b and n > 1 for a, b, n in zip(strides, other, shape)):
         raise ValueError("k_cache and v_cache must have the same strides")
     return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides[:3], *shape), shape
 
@@ -250,6 +250,7 @@ def _attend_plain(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, blo
 
 def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection, scale, window_size,
             out, lse, with_lse, workspace):
+    # selection: () or (block_idx, block_size)
     et, flag, index = _elem(q, "q")
     qs = _strided(q, "q", et, 3, index)
     cache, cshape = _cache_arg(k_cache, v_cache, et, index)
@@ -260,6 +261,12 @@ def _attend(fn, q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, selection
     table = _table_arg(block_table, R, index)
     if d != cshape[3] or cu_seqlens.shape[0] != R + 1:
         raise ValueError("inconsistent shapes")
+    if selection:
+        block_idx, block_size = selection
+        idx = _packed(block_idx, "block_idx", torch.int32, 3, index)
+        if block_idx.shape[:2] != (T, cshape[2]):
+            raise ValueError("inconsistent shapes")
+        selection = idx, block_idx.shape[2], int(block_size)
     if out is None:
         out = q.new_empty(shape)
         to = out.data_ptr()
@@ -318,10 +325,5 @@ def nsa_sel_paged_sel_fwd(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
                         block_size, scale, window_size, out, lse, with_lse, workspace) if block_idx is not None else None
     if got is not None:
         return got
-    idx = _packed(block_idx, "block_idx", torch.int32, 3, _elem(q, "q")[2])
-    rows, heads, topk = block_idx.shape
-    if rows != q.shape[0] or heads != k_cache.shape[2]:
-        raise ValueError("inconsistent shapes")
     return _attend("nsa_sel_paged_sel_fwd", q, k_cache, v_cache, cu_seqlens, kv_lens, block_table,
-                   (idx, topk, int(block_size)), scale, window_size,
-                   out, lse, with_lse, workspace)
+                   (block_idx, block_size), scale, window_size, out, lse, with_lse, workspace)

@@ -181,3 +181,41 @@ def test_plan_refuses_tables_whose_pages_it_cannot_count(lib):
     assert call(8192, 1 << 18) == 2 and call(16384, (1 << 17) - 8) == 2
     if not torch.cuda.is_available():
         assert call(16384, (1 << 17) - 9) in (4, 7)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qs=(0, 128)), dict(qs=(512, 0)), dict(c=cache(page_stride=0)), dict(c=cache(token_stride=0)),
+    dict(c=cache(head_stride=0)), dict(sel=(FAKE, 4, 64), qs=(0, 128))])
+def test_attention_refuses_rows_that_share_memory(lib, kw):
+    assert attend(lib, **kw) == 1
+
+
+def test_write_refuses_cache_rows_that_share_memory(lib):
+    for c in (cache(page_stride=0), cache(token_stride=0), cache(head_stride=0)):
+        assert lib.nsa_sel_paged_write_kv(FAKE, FAKE, 512, 128, 512, 128, FAKE, 3, ctypes.byref(c), None) == 1
+
+
+def test_strides_over_one_place_are_not_looked_at(lib):
+    if torch.cuda.is_available():
+        pytest.skip("fake pointers: only where no device can take the call")
+    one = cache(hkv=1, num_pages=1, head_stride=3, page_stride=-5)
+    assert attend(lib, T=1, hq=1, qs=(5, -3), c=one) in (4, 7)
+    assert attend(lib, T=1, hq=1, qs=(0, 0), c=one, sel=(FAKE, 4, 64)) in (4, 7)
+    assert lib.nsa_sel_paged_write_kv(FAKE, FAKE, 5, 3, -1, 0, FAKE, 1, ctypes.byref(one), None) in (4, 7)
+    # a row repeated for every token or head can be read
+    assert lib.nsa_sel_paged_write_kv(FAKE, FAKE, 0, 0, 512, 0, FAKE, 3, ctypes.byref(cache()), None) in (4, 7)
+
+
+def test_binding_names_what_is_wrong_with_a_selection():
+    q = torch.zeros(1, 4, 128, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    for bad in (None, 3):
+        with pytest.raises((TypeError, ValueError)):
+            nsa.nsa_sel_paged_sel_fwd(q, bad, bad, i, i[:1], i.view(1, 2), i.view(1, 1, 2), 64)
+
+
+def test_strides_of_an_empty_batch_are_not_looked_at(lib):
+    if torch.cuda.is_available():
+        pytest.skip("fake pointers: only where no device can take the call")
+    assert attend(lib, T=0, qs=(0, 0)) in (4, 7) and attend(lib, T=0, qs=(3, -1), sel=(FAKE, 4, 64)) in (4, 7)
+    assert lib.nsa_sel_paged_write_kv(FAKE, FAKE, 0, 3, -1, 0, FAKE, 0, ctypes.byref(cache()), None) in (4, 7)
