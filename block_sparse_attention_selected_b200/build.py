@@ -8,6 +8,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,8 @@ LIB = os.path.join(HERE, "libnsa_sel.so")
 LIB_CHECKS = os.path.join(HERE, "libnsa_sel_checks.so")
 # the compiled marshalling of the paged-cache calls (a Python extension module)
 LIB_BIND = os.path.join(HERE, "_paged_bind.so")
+# ... and what it was built for: the Python and torch whose layouts are compiled into it
+BIND_STAMP = os.path.join(HERE, "_build", "paged_bind.txt")
 SOURCES = ["api.cu", "invert.cu", "fwd.cu", "merge.cu", "bwd.cu", "select.cu", "bsfa.cu",
            "paged.cu", "paged_attn.cu", "paged_few.cu",
            "paged_api.cu"]
@@ -44,14 +47,21 @@ def _stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_target() -> str:
+    """The Python and torch that run now, as _paged_bind.built_for names those it was built for."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__}"
+
+
 def build_bind(force: bool = False) -> str:
     """Builds _paged_bind.so, the compiled marshalling of the paged-cache calls (g++ against the
-    headers of the installed Python and torch)."""
+    headers of the installed Python and torch); again where either has changed."""
     import sysconfig
 
     import torch
     src, header = os.path.join(CSRC, "paged_bind.cpp"), os.path.join(ROOT, "include", "nsa_sel.h")
-    if not force and os.path.exists(LIB_BIND) and \
+    stamp = open(BIND_STAMP).read() if os.path.exists(BIND_STAMP) else ""
+    if not force and stamp == bind_target() and os.path.exists(LIB_BIND) and \
             os.path.getmtime(LIB_BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return LIB_BIND
     base = os.path.dirname(torch.__file__)
@@ -59,21 +69,32 @@ def build_bind(force: bool = False) -> str:
     subprocess.check_call(
         ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         f'-DNSA_BUILT_FOR="{bind_target()}"',
          "-isystem", os.path.join(base, "include"),
          "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
          "-I" + sysconfig.get_paths()["include"], src, "-o", tmp,
          "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
     os.replace(tmp, LIB_BIND)
+    os.makedirs(os.path.dirname(BIND_STAMP), exist_ok=True)
+    with open(BIND_STAMP, "w") as f:
+        f.write(bind_target())
     return LIB_BIND
 
 
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
     """Builds libnsa_sel.so (checks=True: the bounds-checking libnsa_sel_checks.so), and the
-    binding's compiled module."""
-    build_bind(force)
+    binding's compiled module, without which calls go a slower way."""
     lib = LIB_CHECKS if checks else LIB
-    if not force and not _stale(lib):
-        return lib
+    if force or _stale(lib):
+        _build_library(lib, verbose, checks)
+    try:
+        build_bind(force)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"_paged_bind.so was not built, the paged calls are marshalled in Python: {e}")
+    return lib
+
+
+def _build_library(lib: str, verbose: bool, checks: bool) -> None:
     objdir = os.path.join(HERE, "_build_checks" if checks else "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = []
@@ -100,7 +121,6 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     subprocess.check_call([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
                            "-o", tmp, *objs])
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":

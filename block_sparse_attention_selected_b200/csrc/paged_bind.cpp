@@ -216,4 +216,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_bind", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged_bind() { return PyModule_Create(&module); }
+// built_for: the Python and torch whose layouts are compiled in
+PyMODINIT_FUNC PyInit__paged_bind() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", NSA_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -19,6 +19,8 @@ before tokens, K and V as two halves of one tensor) are taken as they are.
 from __future__ import annotations
 
 import ctypes
+import os
+import warnings
 
 import torch
 
@@ -44,9 +46,14 @@ def _plain(t):
     """The compiled module, for a call whose first tensor is t."""
     global _bind
     if _bind is None:
+        from .build import LIB_BIND, bind_target
         try:
             from . import _paged_bind
-        except ImportError:
+            if _paged_bind.built_for != bind_target():
+                raise ImportError(f"it was built for {_paged_bind.built_for}, this is {bind_target()}")
+        except ImportError as e:
+            if os.path.exists(LIB_BIND):       # there, but not for this process
+                warnings.warn(f"_paged_bind.so is not used, the paged calls are marshalled in Python: {e}")
             _bind = False
             return _bind
         lib = load_library()
