@@ -60,7 +60,10 @@ def build_bind(force: bool = False) -> str:
 
     import torch
     src, header = os.path.join(CSRC, "paged_bind.cpp"), os.path.join(ROOT, "include", "nsa_sel.h")
-    stamp = open(BIND_STAMP).read() if os.path.exists(BIND_STAMP) else ""
+    stamp = ""
+    if os.path.exists(BIND_STAMP):
+        with open(BIND_STAMP) as f:
+            stamp = f.read()
     if not force and stamp == bind_target() and os.path.exists(LIB_BIND) and \
             os.path.getmtime(LIB_BIND) >= max(os.path.getmtime(src), os.path.getmtime(header)):
         return LIB_BIND

@@ -33,10 +33,10 @@ __all__ = ["nsa_sel_paged_plan", "nsa_sel_paged_write_kv", "nsa_sel_paged_attn_w
 # host path is kept short: the plain case is marshalled by a small compiled module
 # (csrc/paged_bind.cpp); anything it does not take comes back and is looked at here, where
 # what is wrong gets its name.  The stream and device queries are those that torch's own
-# generated code uses.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# generated code uses (a torch without CUDA lacks them, and has no tensors that get this far).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _ELEM = {torch.bfloat16: 0, torch.float16: NSA_F16}
 
 _bind = None   # the compiled module; False where it was not built

@@ -72,3 +72,23 @@ def test_the_module_that_was_built_is_used(monkeypatch):
     nsa_build.build()
     monkeypatch.setattr(npaged, "_bind", None)
     assert npaged._plain(None) is False and npaged._bind.built_for == nsa_build.bind_target()
+
+
+def test_the_package_imports_where_torch_has_no_cuda():
+    # as a torch that was built without CUDA: importing needs no device and no CUDA binding, and
+    # the calls refuse host tensors by name
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+import block_sparse_attention_selected_b200 as nsa
+i = torch.zeros(1, dtype=torch.int32)
+try:
+    nsa.nsa_sel_paged_plan(i, i, i, i.view(1, 1), 16, 1)
+except ValueError as e:
+    assert "CUDA tensor" in str(e)
+else:
+    raise SystemExit("not refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(nsa.__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
