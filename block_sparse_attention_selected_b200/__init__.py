@@ -170,6 +170,12 @@ def _ws_key(dev: torch.device):
     return (dev, torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _indexed(device) -> torch.device:
+    """The device, the current one where it has no index: "cuda" is the device of its tensors."""
+    dev = torch.device(device)
+    return dev if dev.index is not None else torch.device(dev.type, torch.cuda.current_device())
+
+
 def _capturing(dev: torch.device) -> bool:
     """Whether the device's current stream is being captured into a CUDA graph."""
     if not torch.cuda.is_initialized():
@@ -187,7 +193,7 @@ def get_workspace(nbytes: int, device) -> torch.Tensor:
     graph's own memory and is not cached: a cached buffer would be shared with other graphs
     and with eager calls, which may overlap with a replay, and could be freed under the
     graph.  (nsa_sel_check_status of a replay then needs the call's `workspace`.)"""
-    dev = torch.device(device)
+    dev = _indexed(device)
     if _capturing(dev):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     key = _ws_key(dev)
@@ -463,7 +469,7 @@ def nsa_sel_select_topk(scores, cu_seqlens, block_size, topk, init_blocks=1, loc
 def nsa_sel_check_status(workspace=None, device=None) -> int:
     """Device-side status of the last call that used this workspace (synchronises); by
     default the cached workspace of the device's current stream."""
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    dev = _indexed("cuda" if device is None else device)
     ws = workspace if workspace is not None else _ws_cache.get(_ws_key(dev))
     if ws is None:
         return NSA_OK

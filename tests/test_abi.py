@@ -329,3 +329,18 @@ def test_workspace_of_a_captured_call_is_not_cached(monkeypatch):
     state["capturing"] = False
     assert nsa.get_workspace(100, dev) is eager and list(nsa._ws_cache.values()) == [eager]
     nsa.release_workspaces()
+
+
+def test_workspace_of_cuda_is_that_of_the_current_device(monkeypatch):
+    import types
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda dev=None: types.SimpleNamespace(cuda_stream=11))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    real_empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda n, dtype=None, device=None: real_empty(n, dtype=dtype))
+    nsa.release_workspaces()
+    a = nsa.get_workspace(100, "cuda")
+    assert nsa.get_workspace(50, torch.device("cuda", 1)) is a
+    assert nsa.get_workspace(50, torch.device("cuda", 0)) is not a
+    nsa.release_workspaces()
