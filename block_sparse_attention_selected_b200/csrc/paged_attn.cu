@@ -139,180 +139,180 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // setmaxnreg at the head of each role: the compiler gives the code behind it that many
     if (warp >= kSoftmaxWarps) {
         set_regs_dec<kOtherRegs>();
-    if (warp == 8) {
-        produce<SEL, NQ, Stages>(S, P, wait, &qmap, &kmap, &vmap, lane);
-    } else if (warp != 10) {
-        // ------------------------------------------------------------- MMA issuers
-        // Warp 9 issues for stream 0, warp 11 for stream 1.  A stream's next S follows its
-        // P V on the in-order tensor pipe, which is what lets P share the columns of S.  The
-        // 16 MMAs of an item (a key tile of a stream) are 1024 cycles of tensor work; next to
-        // the busy softmax warps the code around them takes about as long, hence a warp per
-        // stream, everything but P waited for first, addresses that every lane holds through
-        // u() (the compiler then keeps them and all offsets in uniform registers), and a
-        // piece's fields read once.
-        const uint32_t elected = elect_one();
-        constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
-        constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
-        using Kv = Tile<D>;
-        constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
-        constexpr uint32_t kStepU = 2 * Kv::kGroupU;     // 16 keys of V
-        constexpr int step = NQ == 2 ? 1 : 2;
-        auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-        const int st = (int)u(warp == 9 ? 0u : 1u);
-        const uint32_t tS = u(tmem + st * 128u), tO = u(tmem + 256u + st * 128u);
-        const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
-        const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 16, 0));
-        const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 1024, 0));
-        uint64_t *const s_full = &S.s_full[st], *const p_half = &S.p_half[st], *const p_full = &S.p_full[st];
-        uint64_t *const o_full = &S.o_full[st],
-                 *const o_empty = &S.o_empty[st];
-        // two cursors over the pieces: the next S and the next P V; tile numbers over all
-        // pieces give the stages
-        int at_s = -1, js = 0, js_end = 0, base_s = 0, units_s = 0;
-        int at_o = -1, jo = 0, jo_end = 0, base_o = 0;
-        int count_s = 0, count_o = 0;     // key tiles of the pieces so far, both streams
-        bool rows_s = true, rows_o = true;   // the unit has rows in this stream's tile
-        int qb = 0;
-        bool first_o = true;
-        int lo_o = 0, hi_o = 0, tile0_o = 0;
-        int sums = 0, items = 0;          // sums completed, P V items
-        bool ok = true, more_s = true, more_o = true;
-        auto first_tile = [&](int p0, int count) { return NQ == 2 ? p0 : p0 + ((count & 1) ^ st); };
-        // to the next S; everything it waits for.  more_s: there is one
-        auto prepare_s = [&]() -> bool {
-            while (more_s && js >= js_end) {
-                if (!fetch(++at_s)) return false;
-                const Piece& k = S.ring[at_s % kRing];
-                more_s = k.more != 0;
-                const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_s) break;
-                qb = NQ == 2 ? 0 : units_s & 1;
-                ++units_s;
-                js = first_tile(p0, count_s);
-                js_end = p0 + nt;
-                base_s = count_s - p0;
-                count_s += nt;
-                rows_s = NQ == 1 || st == 0 || k.ntok > P.tpt;
-                // (a unit without a tile for this stream is waited for as well, or this
-                // issuer could be done with a later Q of the buffer before the other is with
-                // this one)
-                const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
-                if (!wait(&S.q_full[qb], use & 1)) return false;
-                if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
-            }
-            if (!more_s) return true;
-            const auto to = Stages::k(base_s + js);
-            return wait(&S.kv_full[to.stage], to.phase);
-        };
-        auto issue_s = [&]() {
-            const int stg = Stages::k(base_s + js).stage;
-            const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? st : qb) * kTileU);
-            const uint32_t b0 = u(k_desc0 + (uint32_t)stg * kTileU);
-            if (rows_s) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    mma_ss_hi(tS, a0 + (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2), kSw128Sbo1024DescHi,
-                              b0 + (uint32_t)((x >> 2) * Kv::kHalfU + (x & 3) * 2), Kv::kDescHi, kIdescS,
-                              x > 0 ? 1u : 0u, elected);
+        if (warp == 8) {
+            produce<SEL, NQ, Stages>(S, P, wait, &qmap, &kmap, &vmap, lane);
+        } else if (warp != 10) {
+            // ------------------------------------------------------------- MMA issuers
+            // Warp 9 issues for stream 0, warp 11 for stream 1.  A stream's next S follows its
+            // P V on the in-order tensor pipe, which is what lets P share the columns of S.  The
+            // 16 MMAs of an item (a key tile of a stream) are 1024 cycles of tensor work; next to
+            // the busy softmax warps the code around them takes about as long, hence a warp per
+            // stream, everything but P waited for first, addresses that every lane holds through
+            // u() (the compiler then keeps them and all offsets in uniform registers), and a
+            // piece's fields read once.
+            const uint32_t elected = elect_one();
+            constexpr uint32_t kIdescS = idesc_f16kind_f32(F16 != 0, 128, kTileKeys, false, false);
+            constexpr uint32_t kIdescO = idesc_f16kind_f32(F16 != 0, 128, D, false, true);
+            using Kv = Tile<D>;
+            constexpr uint32_t kHalfU = kRegion >> 4, kTileU = kHalves * kHalfU;
+            constexpr uint32_t kStepU = 2 * Kv::kGroupU;     // 16 keys of V
+            constexpr int step = NQ == 2 ? 1 : 2;
+            auto u = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+            const int st = (int)u(warp == 9 ? 0u : 1u);
+            const uint32_t tS = u(tmem + st * 128u), tO = u(tmem + 256u + st * 128u);
+            const uint32_t q_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.q[0][0]), 16, 1024));
+            const uint32_t k_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 16, 0));
+            const uint32_t v_desc0 = u((uint32_t)smem_desc_sw128(smem_u32(S.kv[0]), 1024, 0));
+            uint64_t *const s_full = &S.s_full[st], *const p_half = &S.p_half[st], *const p_full = &S.p_full[st];
+            uint64_t *const o_full = &S.o_full[st],
+                     *const o_empty = &S.o_empty[st];
+            // two cursors over the pieces: the next S and the next P V; tile numbers over all
+            // pieces give the stages
+            int at_s = -1, js = 0, js_end = 0, base_s = 0, units_s = 0;
+            int at_o = -1, jo = 0, jo_end = 0, base_o = 0;
+            int count_s = 0, count_o = 0;     // key tiles of the pieces so far, both streams
+            bool rows_s = true, rows_o = true;   // the unit has rows in this stream's tile
+            int qb = 0;
+            bool first_o = true;
+            int lo_o = 0, hi_o = 0, tile0_o = 0;
+            int sums = 0, items = 0;          // sums completed, P V items
+            bool ok = true, more_s = true, more_o = true;
+            auto first_tile = [&](int p0, int count) { return NQ == 2 ? p0 : p0 + ((count & 1) ^ st); };
+            // to the next S; everything it waits for.  more_s: there is one
+            auto prepare_s = [&]() -> bool {
+                while (more_s && js >= js_end) {
+                    if (!fetch(++at_s)) return false;
+                    const Piece& k = S.ring[at_s % kRing];
+                    more_s = k.more != 0;
+                    const int p0 = k.p0, nt = k.p1 - p0;
+                    if (!more_s) break;
+                    qb = NQ == 2 ? 0 : units_s & 1;
+                    ++units_s;
+                    js = first_tile(p0, count_s);
+                    js_end = p0 + nt;
+                    base_s = count_s - p0;
+                    count_s += nt;
+                    rows_s = NQ == 1 || st == 0 || k.ntok > P.tpt;
+                    // (a unit without a tile for this stream is waited for as well, or this
+                    // issuer could be done with a later Q of the buffer before the other is with
+                    // this one)
+                    const int use = NQ == 2 ? units_s - 1 : (units_s - 1) >> 1;
+                    if (!wait(&S.q_full[qb], use & 1)) return false;
+                    if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
                 }
-            }
-            mma_commit_e(s_full, elected);
-            mma_commit_e(&S.kv_empty[stg], elected);
-            js += step;
-            if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
-        };
-        ok = prepare_s();
-        if (ok && more_s) issue_s();
-        while (ok) {
-            while (more_o && jo >= jo_end) {
-                if (at_o >= 0) release(at_o);
-                if (!(ok = fetch(++at_o))) break;
-                const Piece& k = S.ring[at_o % kRing];
-                more_o = k.more != 0;
-                const int p0 = k.p0, nt = k.p1 - p0;
-                if (!more_o) break;
-                jo = first_tile(p0, count_o);
-                jo_end = p0 + nt;
-                base_o = count_o - p0;
-                count_o += nt;
-                rows_o = NQ == 1 || st == 0 || k.ntok > P.tpt;
-                lo_o = k.lo;
-                hi_o = k.hi;
-                tile0_o = k.tile0;
-                first_o = true;
-            }
-            if (!ok || !more_o) break;
-            const auto from = Stages::v(base_o + jo);
-            const int stg = from.stage;
-            if (!(ok = wait(&S.kv_full[stg], from.phase))) break;
-            // the tile's visible columns; all of them but at a piece's ends
-            int l0, h0, l1, h1;
-            if (SEL) {
-                tile_cols<SEL>(P, S.ring[at_o % kRing], S.list[at_o % kRing], jo, l0, h0, l1, h1);
-            } else {
-                const int key0 = (tile0_o + jo) * kTileKeys;
-                l0 = max(lo_o - key0, 0);
-                h1 = min(hi_o - key0, 127);
-                h0 = min(h1, 63);
-                l1 = max(l0, 64);
-            }
-            const bool full = l0 == 0 && h0 == 63 && l1 == 64 && h1 == 127;
-            if (!full) {
-                // clear the rows of the used 16-key steps that nobody may see (NQ = 2: both
-                // issuers do, each before its own products)
-                uint8_t* v = S.kv[stg];
-                auto clear = [&](int from, int to) { clear_rows<D>(v, from, to, lane); };
-                if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
-                if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (first_o && sums > 0 && !(ok = wait(o_empty, (sums - 1) & 1))) break;
-            if (!(ok = prepare_s())) break;
-            const uint32_t b0 = u(v_desc0 + (uint32_t)stg * kTileU);
-            uint32_t acc = first_o ? 0u : 1u;
-            if (!(ok = wait(p_half, items & 1))) break;
-            tc_fence_after();
-            if (rows_o && full) {         // the first 64 keys while the rows work on the others
+                if (!more_s) return true;
+                const auto to = Stages::k(base_s + js);
+                return wait(&S.kv_full[to.stage], to.phase);
+            };
+            auto issue_s = [&]() {
+                const int stg = Stages::k(base_s + js).stage;
+                const uint32_t a0 = u(q_desc0 + (uint32_t)(NQ == 2 ? st : qb) * kTileU);
+                const uint32_t b0 = u(k_desc0 + (uint32_t)stg * kTileU);
+                if (rows_s) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, x == 0 ? acc : 1u, elected);
-            }
-            if (!(ok = wait(p_full, items & 1))) break;
-            tc_fence_after();
-            if (rows_o && full) {
-#pragma unroll
-                for (int x = 4; x < 8; ++x)
-                    mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, 1u, elected);
-            } else if (rows_o) {
-#pragma unroll 1
-                for (int x = 0; x < kTileKeys / 16; ++x) {
-                    const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
-                                           : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
-                    if (use) {
-                        mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, acc, elected);
-                        acc = 1u;
+                    for (int x = 0; x < D / 16; ++x) {
+                        mma_ss_hi(tS, a0 + (uint32_t)((x >> 2) * kHalfU + (x & 3) * 2), kSw128Sbo1024DescHi,
+                                  b0 + (uint32_t)((x >> 2) * Kv::kHalfU + (x & 3) * 2), Kv::kDescHi, kIdescS,
+                                  x > 0 ? 1u : 0u, elected);
                     }
                 }
+                mma_commit_e(s_full, elected);
+                mma_commit_e(&S.kv_empty[stg], elected);
+                js += step;
+                if (js >= js_end) mma_commit_e(&S.q_empty[qb], elected);
+            };
+            ok = prepare_s();
+            if (ok && more_s) issue_s();
+            while (ok) {
+                while (more_o && jo >= jo_end) {
+                    if (at_o >= 0) release(at_o);
+                    if (!(ok = fetch(++at_o))) break;
+                    const Piece& k = S.ring[at_o % kRing];
+                    more_o = k.more != 0;
+                    const int p0 = k.p0, nt = k.p1 - p0;
+                    if (!more_o) break;
+                    jo = first_tile(p0, count_o);
+                    jo_end = p0 + nt;
+                    base_o = count_o - p0;
+                    count_o += nt;
+                    rows_o = NQ == 1 || st == 0 || k.ntok > P.tpt;
+                    lo_o = k.lo;
+                    hi_o = k.hi;
+                    tile0_o = k.tile0;
+                    first_o = true;
+                }
+                if (!ok || !more_o) break;
+                const auto from = Stages::v(base_o + jo);
+                const int stg = from.stage;
+                if (!(ok = wait(&S.kv_full[stg], from.phase))) break;
+                // the tile's visible columns; all of them but at a piece's ends
+                int l0, h0, l1, h1;
+                if (SEL) {
+                    tile_cols<SEL>(P, S.ring[at_o % kRing], S.list[at_o % kRing], jo, l0, h0, l1, h1);
+                } else {
+                    const int key0 = (tile0_o + jo) * kTileKeys;
+                    l0 = max(lo_o - key0, 0);
+                    h1 = min(hi_o - key0, 127);
+                    h0 = min(h1, 63);
+                    l1 = max(l0, 64);
+                }
+                const bool full = l0 == 0 && h0 == 63 && l1 == 64 && h1 == 127;
+                if (!full) {
+                    // clear the rows of the used 16-key steps that nobody may see (NQ = 2: both
+                    // issuers do, each before its own products)
+                    uint8_t* v = S.kv[stg];
+                    auto clear = [&](int from, int to) { clear_rows<D>(v, from, to, lane); };
+                    if (l0 <= h0) { clear(l0 & ~15, l0); clear(h0 + 1, (h0 + 16) & ~15); }
+                    if (l1 <= h1) { clear(l1 & ~15, l1); clear(h1 + 1, (h1 + 16) & ~15); }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (first_o && sums > 0 && !(ok = wait(o_empty, (sums - 1) & 1))) break;
+                if (!(ok = prepare_s())) break;
+                const uint32_t b0 = u(v_desc0 + (uint32_t)stg * kTileU);
+                uint32_t acc = first_o ? 0u : 1u;
+                if (!(ok = wait(p_half, items & 1))) break;
+                tc_fence_after();
+                if (rows_o && full) {         // the first 64 keys while the rows work on the others
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, x == 0 ? acc : 1u, elected);
+                }
+                if (!(ok = wait(p_full, items & 1))) break;
+                tc_fence_after();
+                if (rows_o && full) {
+#pragma unroll
+                    for (int x = 4; x < 8; ++x)
+                        mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, 1u, elected);
+                } else if (rows_o) {
+#pragma unroll 1
+                    for (int x = 0; x < kTileKeys / 16; ++x) {
+                        const bool use = x < 4 ? (l0 <= h0 && 16 * x + 15 >= l0 && 16 * x <= h0)
+                                               : (l1 <= h1 && 16 * x + 15 >= l1 && 16 * x <= h1);
+                        if (use) {
+                            mma_ts_hi(tO, tS + x * 8u, b0 + x * kStepU, Kv::kDescHi, kIdescO, acc, elected);
+                            acc = 1u;
+                        }
+                    }
+                }
+                first_o = false;
+                mma_commit_e(&S.kv_empty[stg], elected);
+                jo += step;
+                ++items;
+                if (jo >= jo_end) {               // the stream's last item of the unit: O is complete
+                    mma_commit_e(o_full, elected);
+                    ++sums;
+                }
+                if (more_s) issue_s();
             }
-            first_o = false;
-            mma_commit_e(&S.kv_empty[stg], elected);
-            jo += step;
-            ++items;
-            if (jo >= jo_end) {               // the stream's last item of the unit: O is complete
-                mma_commit_e(o_full, elected);
-                ++sums;
+            mma_commit_e(&S.drain, elected);
+            {
+                const long long start = clock64();
+                while (!mbar_try_wait(&S.drain, 0) && clock64() - start < kWaitBudgetCycles) {}
             }
-            if (more_s) issue_s();
+        } else {
+            schedule<SEL>(S, P, wait, P.tpu, cta, grid, lane);
         }
-        mma_commit_e(&S.drain, elected);
-        {
-            const long long start = clock64();
-            while (!mbar_try_wait(&S.drain, 0) && clock64() - start < kWaitBudgetCycles) {}
-        }
-    } else {
-        schedule<SEL>(S, P, wait, P.tpu, cta, grid, lane);
-    }
     } else {
         set_regs_inc<kSoftmaxRegs>();
         // ------------------------------------------------------- softmax and epilogue
