@@ -5,8 +5,15 @@
 // time, S = Q K^T, P = 2^(c S - m), O += P V, with the running reference m of each row and
 // the sum l of its weights (c = scale log2 e).  m follows the row's maximum lazily: O and
 // l are rescaled only when the maximum has grown by more than 2^8 (kLazy), so that P stays
-// below 2^8 and fp32 sums lose nothing.  P is rounded to the 16-bit type of V for the
-// second product; l sums the unrounded weights.
+// below 2^8 and fp32 sums lose nothing.
+//
+// P is rounded to the 16-bit type of V for the second product, whose operands have one type: half
+// a step (2^-9 in bf16) per weight, independent from key to key, which on rows of many like
+// weights adds about as much as the rounding of the output does (relative error against 64 bits
+// 2.3e-3, of the output's rounding alone 1.7e-3).  l sums the unrounded weights: it gives the lse
+// too, which keeps 32 bits that way (error below 1e-7).  (The packed forward divides by the sum
+// of the rounded weights and keeps a second sum for its lse: a row that one key dominates then
+// has that key's V to one rounding, here to two.)
 //
 // (paged_attn.cuh: units, their division among the CTAs, the scheduler and the producer.)
 // Two streams of (S, P, O) alternate on the tensor pipe, so that one stream's softmax runs
@@ -23,9 +30,9 @@
 //                them over through a ring in shared memory
 //
 // What bounds it.  A chunk of 2048 tokens behind 30720 cached ones (32 query over 8 KV heads,
-// d = 128) takes 945 us (920 - 1040 on other GPUs: the clock), 1.13 PFLOP/s, 68 % of the measured
-// burst rate of a library product of bf16 matrices; called back to back it settles at 0.96 PFLOP/s with the clock (power), 69 %
-// of that product's sustained rate.  Per pair of key tiles (four products of 512 tensor
+// d = 128) takes 917 us, 1.16 PFLOP/s, 70 % of the measured burst rate of a library product of
+// bf16 matrices, in runs too short for the power limit; a call among others takes 1072 - 1092 us,
+// 0.98 PFLOP/s, 71 % of that product's sustained rate (the clock falls).  Per pair of key tiles (four products of 512 tensor
 // cycles) a stream's chain is about 1900 cycles of softmax (S from TMEM 310, maximum 350,
 // exponentials 1200 of which the special-function unit needs 1024) and 1000 - 1700 of its two
 // products.  Measured and not taken: four softmax warpgroups with two threads a row (1016 us:
@@ -33,8 +40,10 @@
 // by polynomial (972 - 1285 us); S in halves of 64 keys (fewer cycles, but Q is read twice a
 // tile and the clock falls: 1010 us); weights formed before the maximum is known (1040 us);
 // one issuer warp for both streams (957 us); the special warps last in the block (1170 us).
-// 16 requests of 3 - 9 tokens on pages of 16: 56 us, 4.0 TB/s; long caches 5.8 TB/s (pages of 64:
+// 16 requests of 3 - 9 tokens on pages of 16: 55 us, 4.1 TB/s; long caches 5.8 TB/s (pages of 64:
 // 6.6), bound by the issue of TMA boxes, one a page.
+// Registers: 4 bytes a thread are spilled; 20, read back at 92 places, in the instances for
+// selected blocks of more than 16 query heads per KV head.
 #include <algorithm>
 #include <type_traits>
 
@@ -631,6 +640,11 @@ bool two_tiles(const PagedAttnArgs& p) { return (long long)p.T * p.G > 128ll * p
 // blocks, 67 against 67 us, a chunk of 512 such tokens 305 against 349 us.  The same kernel
 // with 32 rows lost (16 requests of 3 - 9 tokens, 24 rows on average: 92 against 66 us): its
 // Q and P^T leave room for two thirds of the K / V stages only.
+// Both rules go by the batch's average, padding rows included, since the lengths are on the
+// device: a batch of single tokens and one chunk has one kernel for both, at a price.  32 query
+// over 8 KV heads, contexts to 16384, the chunk's 32768: 63 tokens and a chunk of 128 773 us
+// (apart 363 + 94), 255 and 512 2959 us (1286 + 258), 63 and 2048 1549 us (341 + 1043).  A server
+// that has the lengths on the host makes two calls.
 bool few_rows(const PagedAttnArgs& p) {
     return (p.bidx ? p.G : std::max<long long>(p.G, (long long)p.T * p.G / p.R)) <= kFewRows;
 }

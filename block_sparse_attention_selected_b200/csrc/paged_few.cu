@@ -21,9 +21,12 @@
 // What bounds it: memory, or what lies before it.  64 requests of one token (4 query heads per
 // KV head, 512 to 32768 keys, 4.36 GB of K and V): 635 us, 6.9 TB/s.  One request of 8192 keys:
 // 18 us, of which the data need 5; the rest is the scheduler's first piece and the
-// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 63 us,
-// 4.3 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 297 us, 7.2 TB/s, 28 bytes a cycle and SM,
-// near what the TMA unit takes in.
+// first page lookup, each a chain of loads, and the merge.  Selected blocks of 64 requests: 62 us,
+// 4.4 TB/s; a chunk of 512 tokens, 2.1 GB out of L2: 288 us, 7.5 TB/s, 26 bytes a cycle and SM
+// over the whole call, near the 28 that the TMA unit takes in.  These two change by a few per cent
+// with the size of the code (selected blocks of the chunk: 288 - 334 us with longer and longer
+// wait loops), so what every wait carries is kept short.
+// P^T is rounded to the type of V and l sums the unrounded weights, as in paged_attn.cu.
 //
 //   warps 0-7    softmax and epilogue: a warpgroup per stream, one thread per key of the tile
 //                (per value column in the epilogue)
