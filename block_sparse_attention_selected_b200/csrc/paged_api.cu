@@ -14,14 +14,15 @@ bool stride_ok(int64_t x, int64_t size, int64_t least) { return size <= 1 || (x 
 
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
-nsa_status_t check_cache(const nsa_paged_cache_t* c) {
+// least_stride: 0 where rows are read (one row may stand for many), 1 where they are written.
+nsa_status_t check_cache(const nsa_paged_cache_t* c, int64_t least_stride) {
     if (!c || !c->k || !c->v) return NSA_ERR_INVALID_ARG;
     if (c->num_pages < 1 || c->hkv < 1 || c->head_dim < 1 || c->page_size < 1) return NSA_ERR_INVALID_ARG;
     if (!page_size_ok(c->page_size) || (c->head_dim != 64 && c->head_dim != 128))
         return NSA_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return NSA_ERR_INVALID_ARG;
-    if (!stride_ok(c->page_stride, c->num_pages, 1) || !stride_ok(c->token_stride, c->page_size, 1) ||
-        !stride_ok(c->head_stride, c->hkv, 1))
+    if (!stride_ok(c->page_stride, c->num_pages, least_stride) ||
+        !stride_ok(c->token_stride, c->page_size, least_stride) || !stride_ok(c->head_stride, c->hkv, least_stride))
         return NSA_ERR_INVALID_ARG;
     return NSA_OK;
 }
@@ -31,7 +32,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
                        const int32_t* table, int width, int64_t table_stride, const int32_t* bidx,
                        int topk, int bs, float scale, int swin, void* out, float* lse, void* ws,
                        size_t ws_bytes, nsa_stream_t stream_, unsigned flags) {
-    nsa_status_t s = check_cache(c);
+    nsa_status_t s = check_cache(c, 0);
     if (s != NSA_OK) return s;
     if (flags & ~(unsigned)(NSA_F16 | NSA_TEST_SKIP_ARRIVE)) return NSA_ERR_INVALID_ARG;
     if (T < 0 || hq < 1 || R < 1 || width < 1 || table_stride < width || hq % c->hkv != 0)
@@ -43,7 +44,7 @@ nsa_status_t attn_impl(const void* q, int64_t q_token_stride, int64_t q_head_str
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu, 4) ||
         !aligned(kv_lens, 4) || !aligned(table, 4) || !aligned(bidx, 4) || !aligned(ws, 256))
         return NSA_ERR_INVALID_ARG;
-    if (T > 0 && (!stride_ok(q_token_stride, T, 1) || !stride_ok(q_head_stride, hq, 1)))
+    if (T > 0 && (!stride_ok(q_token_stride, T, 0) || !stride_ok(q_head_stride, hq, 0)))
         return NSA_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !(scale < 1e30f) || swin < 0) return NSA_ERR_INVALID_ARG;
     if (ws_bytes < nsa_sel_paged_attn_workspace_size(T, R, hq, c->hkv, c->head_dim))
@@ -143,7 +144,7 @@ nsa_status_t nsa_sel_paged_write_kv(const void* k, const void* v, int64_t k_toke
                                     int64_t k_head_stride, int64_t v_token_stride,
                                     int64_t v_head_stride, const int64_t* slots, int total_tokens,
                                     const nsa_paged_cache_t* cache, nsa_stream_t stream) {
-    nsa_status_t s = check_cache(cache);
+    nsa_status_t s = check_cache(cache, 1);
     if (s != NSA_OK) return s;
     if (total_tokens < 0) return NSA_ERR_INVALID_ARG;
     if (total_tokens >= (1 << 25)) return NSA_ERR_UNSUPPORTED;

@@ -691,7 +691,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int f16, int num_sms, cuda
     }
     CUtensorMap qmap, kmap, vmap;
     const cuuint64_t qdims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.hq, (cuuint64_t)a.T};
-    // (a dimension of one element may have any stride; the map wants one that is not 0)
+    // (a dimension of one element may have any stride; the map wants multiples of 16 bytes)
     auto stride = [&](long long elems, long long size) {
         return (cuuint64_t)(size > 1 ? elems : a.d) * 2;
     };

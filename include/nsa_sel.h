@@ -342,8 +342,9 @@ NSA_API nsa_status_t nsa_sel_bsfa_fwd(const void *q, const void *k, const void *
  *
  * The cache of one layer: element (page, token in page, KV head, column) of K lies at
  * k + page * page_stride + token * token_stride + head * head_stride + column, V likewise
- * with the same strides.  Strides count elements of 16 bits and are positive multiples of 8
- * (here and below, the stride of a dimension of one element is not looked at);
+ * with the same strides.  Strides count elements of 16 bits and are multiples of 8, not
+ * negative (here and below, the stride of a dimension of one element is not looked at); a stride
+ * of 0, one row in many places, is for the attention calls only;
  * k and v are 16-byte aligned; columns are adjacent.  (A [num_pages, page_size, hkv,
  * head_dim] tensor, the same with heads before tokens, and one half of a tensor holding K
  * and V side by side are all described this way.)
@@ -387,7 +388,7 @@ NSA_API nsa_status_t nsa_sel_paged_plan(const int32_t *new_lens, const int32_t *
 
 /* Writes the K and V rows of total_tokens tokens into their slots.
  *   k, v   16-bit [total_tokens, hkv, head_dim] (the type is not looked at), columns
- *          adjacent, strides in elements, multiples of 8 (0 repeats a row); 16-byte aligned
+ *          adjacent, strides in elements, multiples of 8; 16-byte aligned
  *   slots  int64 [total_tokens]; rows whose slot lies outside [0, num_pages * page_size)
  *          are not written.  Slots that are written must be distinct. */
 NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_t k_token_stride,
@@ -404,7 +405,7 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  * lse = -inf.  Rows of q outside [cu_seqlens[0], cu_seqlens[num_seqs]) are not read and
  * their outputs are left as they were.
  *   q            bf16 (fp16 with flags = NSA_F16) [total_tokens, hq, head_dim], columns
- *                adjacent, strides in elements, positive multiples of 8; 16-byte aligned
+ *                adjacent, strides in elements, multiples of 8; 16-byte aligned
  *   hq           a multiple of cache->hkv, at most 128 query heads per KV head
  *   cu_seqlens   int32 [num_seqs + 1]; kv_lens int32 [num_seqs]
  *   block_table  int32 [num_seqs, table_width], row stride table_stride (elements).  Only

@@ -58,16 +58,25 @@ def test_a_row_repeated_is_written_for_every_token():
     assert torch.equal(vc.view(32, 2, 64)[at], row[:, :1].expand(3, 2, 64))
 
 
-def test_rows_that_share_memory_are_refused():
-    c = make_case([2, 1], [100, 40], 4, 2, 64, 16, seed=2, poison=False)
+@pytest.mark.parametrize("topk", [0, 4])
+def test_attention_reads_one_row_for_many(topk):
+    c = make_case([2, 1, 40], [100, 40, 300], 4, 2, 64, 16, seed=2, topk=topk, poison=False)
     q, k, v, cu, kv, table = tensors(c)
-    wide = [(q[:1].expand(q.shape), k, v), (q[:, :1].expand(q.shape), k, v),
-            (q, k[:1].expand(k.shape), v[:1].expand(v.shape)), (q, k[:, :, :1].expand(k.shape), v[:, :, :1].expand(v.shape))]
-    for a, b, e in wide:
+    for a, b, e in [(q[:1].expand(q.shape), k, v), (q[:, :1].expand(q.shape), k, v),
+                    (q, k[:1].expand(k.shape), v[:1].expand(v.shape)),
+                    (q, k[:, :1].expand(k.shape), v[:, :1].expand(v.shape)),
+                    (q, k[:, :, :1].expand(k.shape), v[:, :, :1].expand(v.shape))]:
+        want = attend(c, (a.contiguous(), b.contiguous(), e.contiguous(), cu, kv, table))
+        got = attend(c, (a, b, e, cu, kv, table))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert nsa.nsa_sel_check_status() == 0
+
+
+def test_write_refuses_cache_rows_that_share_memory():
+    k, v = (torch.randn(3, 2, 64, device="cuda").half() for _ in range(2))
+    c = torch.zeros(4, 16, 2, 64, device="cuda", dtype=torch.float16)
+    for one in (c[:1], c[:, :1], c[:, :, :1]):
         with pytest.raises(nsa.NsaError) as err:
-            nsa.nsa_sel_paged_attn_fwd(a, b, e, cu, kv, table)
+            nsa.nsa_sel_paged_write_kv(k, v, torch.arange(3, device="cuda"), one.expand(c.shape), one.expand(c.shape))
         assert err.value.code == 1
-    with pytest.raises(nsa.NsaError) as err:
-        nsa.nsa_sel_paged_write_kv(q[:, :2], q[:, 2:], torch.arange(3, device="cuda"), k[:1].expand(k.shape),
-                                   v[:1].expand(v.shape))
-    assert err.value.code == 1
+    assert not c.any()
