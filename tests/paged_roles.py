@@ -2,7 +2,8 @@
 two softmax streams, with their mbarriers, the ring of pieces, the K / V stages and the buffers
 of Q, S, P and O, run under random schedules.
 
-It follows csrc/paged_attn.cuh, paged_attn.cu and paged_few.cu wait by wait.  A barrier is a
+It follows the waits between the roles in csrc/paged_attn.cuh, paged_attn.cu and paged_few.cu
+(those among the warps of one stream are left out).  A barrier is a
 count and a phase, a wait looks at the phase's parity only (so a waiter that is two phases off
 passes, as on the device), copies and tensor-core work finish in any order that the device
 allows, and every buffer remembers what it holds: a role that reads something else fails an
