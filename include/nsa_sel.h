@@ -415,15 +415,16 @@ NSA_API nsa_status_t nsa_sel_paged_write_kv(const void *k, const void *v, int64_
  *   lse          fp32 [hq, total_tokens] (written; natural log), or null
  *   workspace    of nsa_sel_paged_attn_workspace_size() bytes (0: unsupported sizes; else
  *                it depends on head_dim alone), 256-byte aligned, contents arbitrary; calls
- *                that may overlap on the GPU need a workspace each
+ *                that may overlap on the GPU need a workspace each.  (Threads may share a stream
+ *                and a workspace: a call's launches are not interleaved with another's.)
  * Cache rows that hold no visible key may hold anything, infinities and NaN too.  (A
  * non-finite V row that some query of a request sees can also reach the outputs of that
  * request's queries of the same KV head that do not see it: 0 times infinity in a shared
  * product.)  The scale must be positive and finite.
- * Test-only flag NSA_TEST_SKIP_ARRIVE: an arrival is missing for the first CTA's first tile of K: the
- * wait for the tile expires after about a second, the CTA lets its copies and tensor-core work end, the call records
- * NSA_ERR_TIMEOUT with undefined outputs, and the device stays usable.  Other flag bits return
- * NSA_ERR_INVALID_ARG.
+ * Test-only flag NSA_TEST_SKIP_ARRIVE: an arrival is missing for the first CTA's first tile of
+ * K.  The wait for the tile expires after about a second, the CTA lets its copies and tensor-core
+ * work end, the call records NSA_ERR_TIMEOUT with undefined outputs, and the device stays usable.
+ * Other flag bits return NSA_ERR_INVALID_ARG.
  * Device-side problems (nsa_sel_check_status): cu_seqlens decreasing or beyond
  * total_tokens, kv_lens beyond the table's row, a used table entry outside [0, num_pages):
  * NSA_ERR_BAD_INDEX, the outputs of that request undefined (of every request, where decreasing
